@@ -274,6 +274,189 @@ int w4a16_decode_step(const w4a16_linear *lin, int64_t n_layers, const uint16_t 
                       hipStream_t stream);
 
 /*
+ * Operators of a decoder layer in 8 bits.  8-bit values are OCP e4m3 codes
+ * (largest finite value 448; one NaN per sign; no infinities), one per byte.
+ */
+
+/*
+ * h = x + residual;  y = weight * h / sqrt(mean(h^2) + eps), per row: the
+ * residual stream's addition and the RMS norm after it.  h stays in fp32 for
+ * the norm; `sum` receives its fp16 rounding (the new residual stream).
+ *
+ *   x         device fp16 rows of ldx elements, [M, width] read.
+ *   residual  device fp16 rows of ldr elements, or NULL (h = x).
+ *   weight    device fp16 [width], or NULL (1).
+ *   eps       >= 0, finite.
+ *   M, width  M in [0, 2^20] rows (0: no-op); width a multiple of 8, at most
+ *             32768.
+ *   sum       device fp16 [M, width], or NULL.  May be x or residual itself
+ *             where that is dense (the update in place); no other overlap.
+ *   y         device fp16 [M, width]; or NULL, and
+ *   y8, y8_scales  device e4m3 [M, width] and fp32 [M, ceil(width / 128)]: per
+ *             row and block of 128 columns (the last may be short),
+ *             s = max(amax, 2^-40) / 448 and y8 = e4m3(y / s), rounded to
+ *             nearest even from fp32.  Exactly one of y and (y8, y8_scales) is
+ *             given.  A row with a NaN comes back as NaN, one with an infinity
+ *             as NaN there and zero elsewhere, as the formula has it.
+ * Errors: INVALID_ARG for NULL x, bad sizes or strides, both or neither
+ * output, overlaps; UNSUPPORTED for width > 32768, M > 2^20, strides of 2^31
+ * or more, pointers that are not 16-byte aligned (scales: 4-byte); HIP on
+ * launch failure.
+ */
+int w4a16_add_rmsnorm(const uint16_t *x, int64_t ldx, const uint16_t *residual, int64_t ldr, const uint16_t *weight,
+                      float eps, int64_t M, int64_t width, uint16_t *sum, uint16_t *y, uint8_t *y8, float *y8_scales,
+                      hipStream_t stream);
+
+/* What w4a16_quant_fp8 applies before it quantises. */
+typedef enum {
+    W4A16_ACT_NONE = 0,   /* t = x[:, :K]                           */
+    W4A16_ACT_SWIGLU = 1  /* t = silu(x[:, :K]) * x[:, K:2K], fp32  */
+} w4a16_act;
+
+/*
+ * Rows to 8 bits with a scale per row and block of 128 columns, as for
+ * w4a16_add_rmsnorm's y8: the input of an 8-bit linear (an attention output;
+ * with SWIGLU, the gate and up projections' output for the down projection).
+ *   x   device fp16 rows of ldx elements (ldx a multiple of 8), [M, K] read
+ *       (SWIGLU: [M, 2K], gate first).
+ *   K   a multiple of 8, at most 2^26; M in [0, 2^20] (0: no-op).
+ *   y8, y8_scales  device e4m3 [M, K] and fp32 [M, ceil(K / 128)].
+ * A block that holds an infinity or a NaN comes back with NaN in it.
+ * Errors: as for w4a16_add_rmsnorm; UNSUPPORTED beyond one launch
+ * (M * ceil(K / 2048) > 2^24).
+ */
+int w4a16_quant_fp8(int act, const uint16_t *x, int64_t ldx, int64_t M, int64_t K, uint8_t *y8, float *y8_scales,
+                    hipStream_t stream);
+
+/*
+ * out[m][n] = sum_b a_scales[m][b] * b_scales[n / 128][b]
+ *                   * sum_{k in block b} a[m][k] * b[n][k],
+ * blocks b of 128 along K (the last may be short): an 8-bit linear whose
+ * activations carry a scale per row and block, and whose weights a scale per
+ * 128 x 128 block.  Products are summed by the 8-bit matrix instructions, whose
+ * inner sums of eight consecutive k cut each product below 2^-14 of the largest
+ * of the eight; everything after that is fp32, with one rounding to fp16.  The
+ * order of the sums depends on the sizes alone: results repeat bit for bit.
+ *
+ *   a         device e4m3 [M, K];  a_scales  device fp32 [M, ceil(K / 128)].
+ *   b         device e4m3 [N, K] (the checkpoint's own order, no repack);
+ *   b_scales  device fp32 [ceil(N / 128), ceil(K / 128)].
+ *   out       device fp16 [M, N], not overlapping an input.
+ *   M >= 0 (0: no-op), K a multiple of 16, any N.
+ * NaN codes and non-finite scales propagate to the outputs they enter.
+ * Errors: INVALID_ARG for NULL pointers, sizes <= 0 (M < 0), overlap;
+ * UNSUPPORTED for K % 16 != 0, pointers that are not 16-byte aligned (scales:
+ * 4-byte), M > 2^20, K or N > 2^26; HIP on launch failure.
+ */
+int w4a16_gemm_fp8(const uint8_t *a, const float *a_scales, const uint8_t *b, const float *b_scales, int64_t M,
+                   int64_t K, int64_t N, uint16_t *out, hipStream_t stream);
+
+/*
+ * A paged key/value cache in 8 bits (host struct; pointers are device).  A
+ * page holds `page` consecutive tokens of one sequence, for every head; each
+ * (page, head) has one scale for its keys and one for its values, a power of
+ * two 2^(byte - 127) with byte in [112, 135].  Every value the cache stands
+ * for is an fp16 value.
+ */
+typedef struct {
+    uint8_t *k;        /* e4m3 [pages, heads, page, dim]  */
+    uint8_t *v;        /* e4m3 [pages, heads, dim, page]: transposed in each page */
+    uint8_t *k_scale;  /* [pages, heads] */
+    uint8_t *v_scale;  /* [pages, heads] */
+    int64_t pages, heads, page, dim; /* page 16, 32, 64, 128 or 256; dim 64, 128 or 256 */
+} w4a16_kv_cache;
+
+/*
+ * Appends a call's keys and values to the cache.  Sequence b's rows are
+ * rows[b] .. rows[b + 1) of k and v (rows == NULL: row b), and they are the
+ * last of its lens[b] positions: position p goes to slot p % page of page
+ * block_table[b][p / page].
+ *   scale  2^e, e = clamp(ceil(log2(amax / 448)), -15, 8), amax over the rows
+ *          of this call that fall into the (page, head); where the page holds
+ *          earlier positions of the sequence, e is at least theirs, and if it
+ *          grows their codes are requantised (a shift of the exponent, rounded
+ *          only below e4m3's normal range).
+ *   codes  e4m3(x / 2^e); at e = 8 they stop at +-240 (61440).  Infinities
+ *          and NaN are stored as NaN and do not enter amax.
+ * Slots of other positions are left as they are.  A page that a call writes
+ * must belong to one sequence (copy a shared one first).  Rows before position
+ * 0 (lens[b] smaller than the sequence's row count), positions past
+ * max_pages * page and pages outside [0, pages) are skipped.
+ *
+ *   k, v         device fp16 rows of ldk / ldv elements (multiples of 8),
+ *                [T, heads * dim] read: columns of a fused projection's output
+ *                may be passed as they are.
+ *   block_table  device int32 [B, max_pages]; lens device int32 [B], the
+ *                lengths with this call's rows; rows device int32 [B + 1],
+ *                non-decreasing from 0 to at most T, or NULL (then T == B).
+ * Errors: INVALID_ARG for NULL pointers, bad sizes or strides, overlap of the
+ * cache's arrays with each other or an input; UNSUPPORTED for other dim or
+ * page sizes, more than 1024 heads, 2^20 rows or sequences, block_table rows of
+ * over 2^30 tokens, pointers that are not 16-byte aligned (the int32 arrays:
+ * 4-byte; scales: any); HIP on launch failure.  T == 0 is a no-op.
+ */
+int w4a16_kv_append(const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv, const w4a16_kv_cache *cache,
+                    const int32_t *block_table, int64_t max_pages, const int32_t *lens, const int32_t *rows, int64_t B,
+                    int64_t T, hipStream_t stream);
+
+/*
+ * Causal attention over the cache, for single tokens and for prompts:
+ *     out_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale * q_i . k_j)
+ * over the positions j <= pos_i of the row's sequence, with window > 0 only
+ * j > pos_i - window.  Rows, lens and block_table as for w4a16_kv_append (the
+ * rows' own keys and values are in the cache already).  Query head h reads
+ * cache head h / (heads / cache->heads).
+ *   q      device fp16 rows of ldq elements (a multiple of 8),
+ *          [T, heads * dim] read.
+ *   out    device fp16 [T, heads * dim].  Rows past rows[B] are left as they
+ *          are.  A row that sees no position (before position 0) is zero.  NaN
+ *          reaches exactly the rows that see it, whatever lies in masked or
+ *          unused slots.  A row at or past position max_pages * page, or that
+ *          sees a page outside [0, pages), is NaN.
+ *   workspace  device scratch of w4a16_attention_workspace_bytes() bytes
+ *          (NULL where that is 0), caller-owned, not shared with a call that
+ *          may run at the same time; nothing in it need be initialised.
+ * Scores and softmax are fp32; the weights are rounded to fp16 for the product
+ * with the values.  The order of the sums depends on the sizes alone (B, T,
+ * max_pages) and lens, so results repeat bit for bit.
+ * Errors: as for w4a16_kv_append; INVALID_ARG also for heads that are no
+ * multiple of the cache's, a scale that is not finite, window < 0, a short
+ * workspace, or out or workspace overlapping anything else; UNSUPPORTED for
+ * more than 1024 query heads or rows and heads past one launch.
+ */
+size_t w4a16_attention_workspace_bytes(int64_t heads, const w4a16_kv_cache *cache, int64_t max_pages, int64_t B,
+                                       int64_t T);
+int w4a16_attention(const uint16_t *q, int64_t ldq, int64_t heads, const w4a16_kv_cache *cache,
+                    const int32_t *block_table, int64_t max_pages, const int32_t *lens, const int32_t *rows, int64_t B,
+                    int64_t T, float scale, int64_t window, uint16_t *out, void *workspace, size_t workspace_bytes,
+                    hipStream_t stream);
+
+/*
+ * w4a16_decode_step with attention in the place of its stand-in: one token for
+ * each of M sequences, the first linear's output holding queries, keys and
+ * values (N = H + 2 * cache heads * dim, in that order; H = query heads * dim).
+ * With the workspace's three buffers P, Q, R (as for w4a16_decode_step) the
+ * step is exactly
+ *     layer 0:   w4a16_gemm_glue(NONE, x_in, H, qkv)          -> P
+ *     layer l>0: w4a16_gemm_glue(RMSNORM, R, H, qkv)          -> P
+ *                w4a16_kv_append(P + H, P + H + heads * dim)  -> caches[l]
+ *                w4a16_attention(P, caches[l], scale)         -> Q
+ *                w4a16_gemm_glue(NONE, Q, H, o)               -> R
+ *                w4a16_gemm_glue(RMSNORM, R, H, gate_up)      -> P
+ *                w4a16_gemm_glue(SWIGLU, P, 2I, down)         -> R
+ *     then       w4a16_rownorm(R, H, M, H)                    -> x_out
+ *   caches  host array of n_layers caches; block_table and lens (with this
+ *           token) are shared by the layers.
+ * Errors: as for w4a16_decode_step, w4a16_kv_append and w4a16_attention.
+ */
+size_t w4a16_decode_kv_workspace_bytes(int64_t M, const w4a16_linear *lin, int64_t n_layers,
+                                       const w4a16_kv_cache *caches, int64_t max_pages);
+int w4a16_decode_step_kv(const w4a16_linear *lin, int64_t n_layers, const w4a16_kv_cache *caches,
+                         const int32_t *block_table, int64_t max_pages, const int32_t *lens, float scale,
+                         const uint16_t *x_in, uint16_t *x_out, int64_t M, void *workspace, size_t workspace_bytes,
+                         hipStream_t stream);
+
+/*
  * Describe the plan w4a16_gemm would run for a shape (host-only, no HIP calls):
  * path 1 = GEMV on the vector ALUs (dot2), 3 = GEMV with its k-reduction on
  * the matrix cores (M <= 8, the default there), 2 = MFMA GEMM (tiles of 16+

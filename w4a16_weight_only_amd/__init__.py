@@ -10,6 +10,15 @@ the library is missing or the tensors are not on the GPU, the call raises.
     out = w4a16_gemm(a, b_packed, scales, qzeros, G, zp_bias=8)
     dst = w4a16_repack(src_nk8, K)
     y   = w4a16_decode_step(stack, x)
+
+The operators around the linears of a decoder layer, in 8 bits (OCP e4m3):
+
+    cache = w4a16_kv_cache(pages, heads, page, dim)
+    w4a16_kv_append(k, v, cache, block_table, lens, rows)
+    out = w4a16_attention(q, cache, block_table, lens, rows)
+    (codes, scales), x = w4a16_add_rmsnorm_fp8(x, residual, weight)
+    codes, scales = w4a16_quant_fp8(gate_up, ACT_SWIGLU)
+    out = w4a16_gemm_fp8(codes, scales, w_codes, w_scales)
 """
 from __future__ import annotations
 
@@ -21,6 +30,9 @@ __all__ = [
     "w4a16_decode_workspace_bytes", "w4a16_gemm_glue", "w4a16_gemm_glue_workspace_bytes", "w4a16_rownorm",
     "w4a16_gemm_plan", "w4a16_set_tuning", "w4a16_release", "Linear", "STATUS",
     "GLUE_NONE", "GLUE_RMSNORM", "GLUE_SWIGLU",
+    "w4a16_add_rmsnorm", "w4a16_add_rmsnorm_fp8", "w4a16_quant_fp8", "w4a16_gemm_fp8", "w4a16_kv_cache",
+    "w4a16_kv_append", "w4a16_attention", "w4a16_attention_workspace_bytes", "w4a16_decode_step_kv",
+    "w4a16_decode_kv_workspace_bytes", "KVCache", "ACT_NONE", "ACT_SWIGLU",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -29,6 +41,7 @@ LIB_PATH = os.path.join(_HERE, "libw4a16.so")
 STATUS = {0: "W4A16_OK", 1: "W4A16_ERR_INVALID_ARG", 2: "W4A16_ERR_UNSUPPORTED",
           3: "W4A16_ERR_HIP", 4: "W4A16_ERR_WORKSPACE"}
 GLUE_NONE, GLUE_RMSNORM, GLUE_SWIGLU = 0, 1, 2
+ACT_NONE, ACT_SWIGLU = 0, 1
 
 
 class W4A16Error(RuntimeError):
@@ -42,6 +55,13 @@ class Linear(ctypes.Structure):
     _fields_ = [("b_packed", ctypes.c_void_p), ("scales", ctypes.c_void_p),
                 ("qzeros", ctypes.c_void_p), ("K", ctypes.c_int64), ("N", ctypes.c_int64),
                 ("G", ctypes.c_int64), ("zp_bias", ctypes.c_int32)]
+
+
+class KVCache(ctypes.Structure):
+    """Mirror of ``w4a16_kv_cache`` (host struct holding device pointers)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int64), ("heads", ctypes.c_int64),
+                ("page", ctypes.c_int64), ("dim", ctypes.c_int64)]
 
 
 _lib = None
@@ -85,6 +105,23 @@ def lib() -> ctypes.CDLL:
     L.w4a16_release.argtypes = []
     L.w4a16_set_tuning.restype = ctypes.c_int
     L.w4a16_set_tuning.argtypes = [ctypes.c_char_p]
+    F32 = ctypes.c_float
+    L.w4a16_add_rmsnorm.restype = ctypes.c_int
+    L.w4a16_add_rmsnorm.argtypes = [P, I64, P, I64, P, F32, I64, I64, P, P, P, P, P]
+    L.w4a16_quant_fp8.restype = ctypes.c_int
+    L.w4a16_quant_fp8.argtypes = [ctypes.c_int, P, I64, I64, I64, P, P, P]
+    L.w4a16_gemm_fp8.restype = ctypes.c_int
+    L.w4a16_gemm_fp8.argtypes = [P, P, P, P, I64, I64, I64, P, P]
+    L.w4a16_kv_append.restype = ctypes.c_int
+    L.w4a16_kv_append.argtypes = [P, I64, P, I64, P, P, I64, P, P, I64, I64, P]
+    L.w4a16_attention_workspace_bytes.restype = SZ
+    L.w4a16_attention_workspace_bytes.argtypes = [I64, P, I64, I64, I64]
+    L.w4a16_attention.restype = ctypes.c_int
+    L.w4a16_attention.argtypes = [P, I64, I64, P, P, I64, P, P, I64, I64, F32, I64, P, P, SZ, P]
+    L.w4a16_decode_kv_workspace_bytes.restype = SZ
+    L.w4a16_decode_kv_workspace_bytes.argtypes = [I64, P, I64, P, I64]
+    L.w4a16_decode_step_kv.restype = ctypes.c_int
+    L.w4a16_decode_step_kv.argtypes = [P, I64, P, P, I64, P, F32, P, P, I64, P, SZ, P]
     _lib = L
     return L
 
@@ -311,3 +348,298 @@ def w4a16_set_tuning(spec=None):
 
 def w4a16_release():
     _check(lib().w4a16_release())
+
+
+# ------------------------------------------- decoder-layer operators, 8 bits ---
+
+def _row_tensor(t, name):
+    """fp16 rows with unit stride along the last dimension; the row stride is free."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype != torch.float16:
+        raise TypeError("%s must be torch.float16, got %s" % (name, t.dtype))
+    if t.dim() != 2:
+        raise ValueError("%s must be 2-D, got shape %s" % (name, tuple(t.shape)))
+    if not t.is_cuda:
+        raise ValueError("%s must be on the GPU" % name)
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError("%s must have unit stride along its last dimension" % name)
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _same_device(first, **others):
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError("%s is on %s, not on %s" % (name, t.device, first.device))
+
+
+def _launch(dev, fn, *args):
+    """fn(*args, stream) on the tensors' device and torch's current stream there."""
+    torch = _torch()
+    if dev.index is not None and dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream_ptr(dev)))
+    else:
+        _check(fn(*args, _stream_ptr(dev)))
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _blocks(n):
+    return -(-n // 128)
+
+
+def _norm_args(x, residual, weight, sum_out):
+    torch = _torch()
+    ldx = _row_tensor(x, "x")
+    M, W = x.shape
+    ldr = 0
+    if residual is not None:
+        ldr = _row_tensor(residual, "residual")
+        if tuple(residual.shape) != (M, W):
+            raise ValueError("residual must be [M, width] = [%d, %d]" % (M, W))
+    if weight is not None:
+        _dev_tensor(weight, "weight", torch.float16, 1)
+        if weight.shape[0] != W:
+            raise ValueError("weight must be [width] = [%d]" % W)
+    if sum_out is None:
+        if residual is not None:
+            sum_out = torch.empty((M, W), dtype=torch.float16, device=x.device)
+    else:
+        _dev_tensor(sum_out, "sum_out", torch.float16, 2)
+        if tuple(sum_out.shape) != (M, W):
+            raise ValueError("sum_out must be [M, width] = [%d, %d]" % (M, W))
+    _same_device(x, residual=residual, weight=weight, sum_out=sum_out)
+    return ldx, ldr, M, W, sum_out
+
+
+def w4a16_add_rmsnorm(x, residual=None, weight=None, eps=1e-6, out=None, sum_out=None):
+    """(y, h): h = x + residual and y = weight * h / sqrt(mean(h^2) + eps), fp16
+    rows [M, width].  sum_out receives h; it may be x or residual itself (the
+    residual stream updated in place).  Without a residual and sum_out, h is x."""
+    torch = _torch()
+    ldx, ldr, M, W, sum_out = _norm_args(x, residual, weight, sum_out)
+    if out is None:
+        out = torch.empty((M, W), dtype=torch.float16, device=x.device)
+    else:
+        _dev_tensor(out, "out", torch.float16, 2)
+        if tuple(out.shape) != (M, W):
+            raise ValueError("out must be [M, width] = [%d, %d]" % (M, W))
+        _same_device(x, out=out)
+    _launch(x.device, lib().w4a16_add_rmsnorm, x.data_ptr(), ldx, _ptr(residual), ldr, _ptr(weight), eps, M, W,
+            _ptr(sum_out), out.data_ptr(), None, None)
+    return out, x if sum_out is None else sum_out
+
+
+def _codes_out(out, M, K, dev):
+    """Output tensors of a quantising call: e4m3 [M, K] and fp32 [M, ceil(K/128)]."""
+    torch = _torch()
+    if out is None:
+        return (torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev),
+                torch.empty((M, _blocks(K)), dtype=torch.float32, device=dev))
+    codes, scales = out
+    _dev_tensor(codes, "codes", torch.float8_e4m3fn, 2)
+    _dev_tensor(scales, "scales", torch.float32, 2)
+    if tuple(codes.shape) != (M, K) or tuple(scales.shape) != (M, _blocks(K)):
+        raise ValueError("out must be codes [%d, %d] and scales [%d, %d]" % (M, K, M, _blocks(K)))
+    return codes, scales
+
+
+def w4a16_add_rmsnorm_fp8(x, residual=None, weight=None, eps=1e-6, out=None, sum_out=None):
+    """((codes, scales), h): as w4a16_add_rmsnorm, with y in e4m3 [M, width] and a
+    scale fp32 [M, ceil(width/128)] per row and block of 128 columns."""
+    ldx, ldr, M, W, sum_out = _norm_args(x, residual, weight, sum_out)
+    codes, scales = _codes_out(out, M, W, x.device)
+    _same_device(x, codes=codes, scales=scales)
+    _launch(x.device, lib().w4a16_add_rmsnorm, x.data_ptr(), ldx, _ptr(residual), ldr, _ptr(weight), eps, M, W,
+            _ptr(sum_out), None, codes.data_ptr(), scales.data_ptr())
+    return (codes, scales), x if sum_out is None else sum_out
+
+
+def w4a16_quant_fp8(x, act=ACT_NONE, out=None):
+    """(codes, scales) of fp16 rows x: ACT_NONE quantises x [M, K], ACT_SWIGLU
+    silu(x[:, :K]) * x[:, K:] of x [M, 2K], to e4m3 [M, K] with a scale fp32
+    [M, ceil(K/128)] per row and block of 128 columns."""
+    ldx = _row_tensor(x, "x")
+    M, K = x.shape
+    if act == ACT_SWIGLU:
+        if K % 2:
+            raise ValueError("SwiGLU takes rows of gate and up halves, got width %d" % K)
+        K //= 2
+    codes, scales = _codes_out(out, M, K, x.device)
+    _same_device(x, codes=codes, scales=scales)
+    _launch(x.device, lib().w4a16_quant_fp8, act, x.data_ptr(), ldx, M, K, codes.data_ptr(), scales.data_ptr())
+    return codes, scales
+
+
+def w4a16_gemm_fp8(a, a_scales, b, b_scales, out=None):
+    """out[M, N] fp16 = A . B^T with A = a (e4m3 [M, K]) scaled by a_scales (fp32
+    [M, ceil(K/128)]) and B = b (e4m3 [N, K]) scaled by b_scales (fp32
+    [ceil(N/128), ceil(K/128)])."""
+    torch = _torch()
+    _dev_tensor(a, "a", torch.float8_e4m3fn, 2)
+    _dev_tensor(a_scales, "a_scales", torch.float32, 2)
+    _dev_tensor(b, "b", torch.float8_e4m3fn, 2)
+    _dev_tensor(b_scales, "b_scales", torch.float32, 2)
+    M, K = a.shape
+    N = b.shape[0]
+    if b.shape[1] != K:
+        raise ValueError("b must be [N, K] = [*, %d], got %s" % (K, tuple(b.shape)))
+    if tuple(a_scales.shape) != (M, _blocks(K)):
+        raise ValueError("a_scales must be [M, ceil(K/128)] = [%d, %d]" % (M, _blocks(K)))
+    if tuple(b_scales.shape) != (_blocks(N), _blocks(K)):
+        raise ValueError("b_scales must be [ceil(N/128), ceil(K/128)] = [%d, %d]" % (_blocks(N), _blocks(K)))
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.float16, device=a.device)
+    else:
+        _dev_tensor(out, "out", torch.float16, 2)
+        if tuple(out.shape) != (M, N):
+            raise ValueError("out must be [M, N] = [%d, %d]" % (M, N))
+    _same_device(a, a_scales=a_scales, b=b, b_scales=b_scales, out=out)
+    _launch(a.device, lib().w4a16_gemm_fp8, a.data_ptr(), a_scales.data_ptr(), b.data_ptr(), b_scales.data_ptr(), M, K,
+            N, out.data_ptr())
+    return out
+
+
+def w4a16_kv_cache(pages, heads, page, dim, device="cuda"):
+    """An empty paged 8-bit key/value cache: a dict of k e4m3 [pages, heads, page,
+    dim], v e4m3 [pages, heads, dim, page] (transposed in each page), and k_scale
+    and v_scale uint8 [pages, heads] (scale 2^(byte - 127))."""
+    torch = _torch()
+    return dict(k=torch.zeros((pages, heads, page, dim), dtype=torch.float8_e4m3fn, device=device),
+                v=torch.zeros((pages, heads, dim, page), dtype=torch.float8_e4m3fn, device=device),
+                k_scale=torch.full((pages, heads), 112, dtype=torch.uint8, device=device),
+                v_scale=torch.full((pages, heads), 112, dtype=torch.uint8, device=device))
+
+
+def _cache_struct(cache):
+    torch = _torch()
+    k, v, ks, vs = cache["k"], cache["v"], cache["k_scale"], cache["v_scale"]
+    _dev_tensor(k, "cache k", torch.float8_e4m3fn, 4)
+    _dev_tensor(v, "cache v", torch.float8_e4m3fn, 4)
+    _dev_tensor(ks, "cache k_scale", torch.uint8, 2)
+    _dev_tensor(vs, "cache v_scale", torch.uint8, 2)
+    P, H, page, D = k.shape
+    if tuple(v.shape) != (P, H, D, page) or tuple(ks.shape) != (P, H) or tuple(vs.shape) != (P, H):
+        raise ValueError("cache must hold k [pages, heads, page, dim], v [pages, heads, dim, page] and scales "
+                         "[pages, heads]")
+    _same_device(k, v=v, k_scale=ks, v_scale=vs)
+    return KVCache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), P, H, page, D)
+
+
+def _sequence_args(block_table, lens, rows, T):
+    torch = _torch()
+    _dev_tensor(block_table, "block_table", torch.int32, 2)
+    _dev_tensor(lens, "lens", torch.int32, 1)
+    B = lens.shape[0]
+    if block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, max_pages] with B = %d" % B)
+    if rows is not None:
+        _dev_tensor(rows, "rows", torch.int32, 1)
+        if rows.shape[0] != B + 1:
+            raise ValueError("rows must be [B + 1] = [%d]" % (B + 1))
+    elif T != B:
+        raise ValueError("without rows there is one row per sequence: %d rows, %d sequences" % (T, B))
+    return B, block_table.shape[1]
+
+
+def w4a16_kv_append(k, v, cache, block_table, lens, rows=None):
+    """Writes fp16 rows k and v [T, heads*dim] (any row stride) to the cache as the
+    last positions of sequences of lens[b] tokens: sequence b's rows are
+    rows[b]..rows[b+1] (rows None: row b), position p goes to slot p % page of
+    page block_table[b, p // page].  Returns the cache."""
+    ldk, ldv = _row_tensor(k, "k"), _row_tensor(v, "v")
+    c = _cache_struct(cache)
+    T, W = k.shape
+    if W != c.heads * c.dim or tuple(v.shape) != (T, W):
+        raise ValueError("k and v must be [T, heads*dim] = [*, %d], got %s and %s"
+                         % (c.heads * c.dim, tuple(k.shape), tuple(v.shape)))
+    B, width = _sequence_args(block_table, lens, rows, T)
+    _same_device(k, v=v, cache=cache["k"], block_table=block_table, lens=lens, rows=rows)
+    _launch(k.device, lib().w4a16_kv_append, k.data_ptr(), ldk, v.data_ptr(), ldv, ctypes.byref(c),
+            block_table.data_ptr(), width, lens.data_ptr(), _ptr(rows), B, T)
+    return cache
+
+
+def w4a16_attention_workspace_bytes(heads, cache, max_pages, B, T):
+    c = _cache_struct(cache)
+    return int(lib().w4a16_attention_workspace_bytes(heads, ctypes.byref(c), max_pages, B, T))
+
+
+def w4a16_attention(q, cache, block_table, lens, rows=None, scale=None, window=0, out=None, workspace=None):
+    """Causal attention of fp16 rows q [T, heads*dim] (any row stride) over the
+    cache; sequences as for w4a16_kv_append, whose rows are in the cache already.
+    scale defaults to 1/sqrt(dim); window > 0 keeps each row's last `window`
+    positions.  Returns fp16 [T, heads*dim]; rows past rows[-1] are not written."""
+    torch = _torch()
+    ldq = _row_tensor(q, "q")
+    c = _cache_struct(cache)
+    T, W = q.shape
+    if W == 0 or W % (c.heads * c.dim):
+        raise ValueError("q must be [T, heads*dim] with heads a multiple of %d and dim %d, got %s"
+                         % (c.heads, c.dim, tuple(q.shape)))
+    heads = W // c.dim
+    B, width = _sequence_args(block_table, lens, rows, T)
+    if out is None:
+        out = torch.empty((T, W), dtype=torch.float16, device=q.device)
+    else:
+        _dev_tensor(out, "out", torch.float16, 2)
+        if tuple(out.shape) != (T, W):
+            raise ValueError("out must be [T, heads*dim] = [%d, %d]" % (T, W))
+    ref = ctypes.byref(c)
+    if workspace is None:
+        need = lib().w4a16_attention_workspace_bytes(heads, ref, width, B, T)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _same_device(q, cache=cache["k"], block_table=block_table, lens=lens, rows=rows, out=out, workspace=workspace)
+    _launch(q.device, lib().w4a16_attention, q.data_ptr(), ldq, heads, ref, block_table.data_ptr(), width,
+            lens.data_ptr(), _ptr(rows), B, T, c.dim ** -0.5 if scale is None else scale, window, out.data_ptr(),
+            _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size())
+    return out
+
+
+def _decode_kv_args(stack, caches, M, max_pages):
+    if len(stack) % 4 != 0 or not stack:
+        raise ValueError("stack must hold 4 linears per layer")
+    if len(caches) != len(stack) // 4:
+        raise ValueError("caches must hold one cache per layer")
+    arr = _linear_array(stack)
+    carr = (KVCache * len(caches))(*[_cache_struct(c) for c in caches])
+    lp, cp = ctypes.cast(arr, ctypes.c_void_p), ctypes.cast(carr, ctypes.c_void_p)
+    need = int(lib().w4a16_decode_kv_workspace_bytes(M, lp, len(caches), cp, max_pages))
+    return arr, carr, lp, cp, need
+
+
+def w4a16_decode_kv_workspace_bytes(M, stack, caches, max_pages):
+    return _decode_kv_args(stack, caches, M, max_pages)[4]
+
+
+def w4a16_decode_step_kv(stack, caches, block_table, lens, x, scale=None, out=None, workspace=None):
+    """One decode step of len(stack)//4 layers with attention over one cache per
+    layer: x fp16 [M, H] holds one token for each of M sequences, lens their
+    lengths with it."""
+    torch = _torch()
+    _dev_tensor(x, "x", torch.float16, 2)
+    M = x.shape[0]
+    _, width = _sequence_args(block_table, lens, None, M)
+    arr, carr, lp, cp, need = _decode_kv_args(stack, caches, M, width)
+    if x.shape[1] != arr[0].K:
+        raise ValueError("x must be [M, H] = [%d, %d]" % (M, arr[0].K))
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _dev_tensor(out, "out", torch.float16, 2)
+        if out.shape != x.shape:
+            raise ValueError("out must be [M, H] = [%d, %d]" % tuple(x.shape))
+    _same_device(x, block_table=block_table, lens=lens, out=out, workspace=workspace,
+                 **{"stack[%d]" % i: L["b_packed"] for i, L in enumerate(stack)},
+                 **{"caches[%d]" % i: c["k"] for i, c in enumerate(caches)})
+    _launch(x.device, lib().w4a16_decode_step_kv, lp, len(caches), cp, block_table.data_ptr(), width, lens.data_ptr(),
+            carr[0].dim ** -0.5 if scale is None else scale, x.data_ptr(), out.data_ptr(), M, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
+    return out

@@ -16,6 +16,7 @@
 
 #include "w4a16.h"
 #include "kernels.h"
+#include "layer.h"
 
 namespace w4a16 {
 int gemv_words_for_m(int64_t M);
@@ -465,6 +466,16 @@ GemmPlan plan_gemm(int64_t M, int64_t K, int64_t N, int64_t G, bool allow_mma, b
         p.counters = p.splits > 1 ? (size_t)(p.tiles_n * p.tiles_m) : 0;
     }
     return p;
+}
+
+}  // namespace w4a16
+
+namespace w4a16 {
+
+int set_error(int status, const std::string &msg) {
+    if (status == W4A16_OK) g_last_error.clear();
+    else g_last_error = msg;
+    return status;
 }
 
 }  // namespace w4a16

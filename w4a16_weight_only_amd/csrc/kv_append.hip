@@ -1,0 +1,157 @@
+// kv_append.hip -- writes a call's keys and values into the paged 8-bit cache.
+//
+// A page of one key/value head holds its tokens' codes and one scale for keys
+// and one for values, each a power of two 2^e:
+//   e = clamp(ceil(log2(amax / 448)), -15, 8) over the page's tokens,
+// never below the e that earlier tokens of the page already have.  Powers of
+// two lose no precision against a free scale (e4m3 is a floating format) and
+// make two things exact: a page whose scale grows has its old codes' exponents
+// shifted, with a rounding only where they fall below e4m3's normal range; and
+// every dequantised value is an fp16 value (at e >= -15 its last bit is worth
+// at least 2^-24, and at e = 8 codes stop at 240, 61440), so attention feeds
+// the matrix cores with no further rounding.  Infinities and NaN are stored as
+// NaN and do not enter amax.
+//
+// Keys are stored [page, dim], values transposed [dim, page]: each is then the
+// order in which attention's matrix instructions take 16 bytes per lane.
+//
+// One workgroup owns one (page, head) of K or of V, so no two touch the same
+// scale: it reads the new rows for amax, again (from cache) to write codes.
+// Bound by HBM for prompts and by latency for single tokens.
+#include "device.h"
+#include "layer.h"
+
+namespace w4a16 {
+namespace {
+
+__device__ __forceinline__ float finite_abs(float x) {
+    const float a = __builtin_fabsf(x);
+    return a < __builtin_inff() ? a : 0.f;  // NaN and infinities: 0
+}
+
+// x / 2^e as e4m3 input: saturated where e is the largest (61440 = 240 * 2^8,
+// the largest code whose value fp16 holds), NaN for infinities.
+__device__ __forceinline__ float scaled(float x, float inv, bool top) {
+    float s = x * inv;
+    if (top) s = __builtin_fabsf(s) < __builtin_inff() ? fminf(fmaxf(s, -240.f), 240.f) : s;
+    return __builtin_fabsf(s) <= 448.f ? s : __builtin_nanf("");
+}
+
+__device__ __forceinline__ float fp8_value(uint32_t code) {
+    return __builtin_amdgcn_cvt_f32_fp8((int)code, 0);
+}
+
+template <int THREADS>
+__global__ __launch_bounds__(THREADS) void kv_append_kernel(const uint16_t *__restrict__ kin, int64_t ldk,
+                                                            const uint16_t *__restrict__ vin, int64_t ldv,
+                                                            CacheArgs c, SeqArgs s) {
+    __shared__ float sh[THREADS / 64];
+    const int page = 1 << c.page_shift, D = c.dim, head = blockIdx.y;
+    const bool is_v = blockIdx.z != 0;
+    // Work item -> (sequence, one of the pages its rows fall into).  Sequence
+    // b's items start at floor(rows[b] / page) + 2b, which leaves room for its
+    // floor(n / page) + 2 or fewer pages.
+    const int64_t id = blockIdx.x;
+    int b;
+    int64_t first_id;
+    if (!s.rows) {
+        b = (int)id;
+        first_id = id;
+    } else {
+        auto start = [&](int i) {
+            int r = s.rows[i];
+            r = r < 0 ? 0 : r > s.T ? s.T : r;
+            return (int64_t)(r >> c.page_shift) + 2 * (int64_t)i;
+        };
+        b = find_sequence(s.B, id, start);
+        first_id = start(b);
+    }
+    int r0, n;
+    sequence_rows(s, b, r0, n);
+    const int64_t len = s.lens[b];
+    const int64_t begin = len - n < 0 ? 0 : len - n;  // first position written
+    const int64_t pg = (begin >> c.page_shift) + (id - first_id);
+    const int64_t p0 = pg << c.page_shift;
+    const int64_t lo = p0 > begin ? p0 : begin, hi = p0 + page < len ? p0 + page : len;
+    if (n == 0 || lo >= hi || pg >= s.max_pages) return;
+    const int64_t pid = s.table[(int64_t)b * s.max_pages + pg];
+    if (pid < 0 || pid >= c.pages) return;
+    const int a = (int)(lo - p0), m = (int)(hi - lo);  // tokens a .. a + m of the page
+    const int64_t row = r0 + (lo - (len - n));         // the first one's input row
+    const uint16_t *in = (is_v ? vin : kin) + (size_t)head * D;
+    const int64_t ld = is_v ? ldv : ldk;
+    const size_t slot = (size_t)pid * c.heads + head;
+    uint8_t *codes = (is_v ? c.v : c.k) + slot * page * D;
+    uint8_t *scale = (is_v ? c.v_scale : c.k_scale) + slot;
+
+    const int vpr = D >> 3;  // 16-byte vectors per row
+    float amax = 0.f;
+    for (int i = threadIdx.x; i < m * vpr; i += THREADS) {
+        const int t = i / vpr, d = (i - t * vpr) * 8;
+        const u32x4 x = *reinterpret_cast<const u32x4 *>(in + (row + t) * ld + d);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            amax = fmaxf(amax, finite_abs(f16_bits_to_f32((x[e >> 1] >> (16 * (e & 1))) & 0xffffu)));
+    }
+#pragma unroll
+    for (int o = 32; o; o >>= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
+    if constexpr (THREADS > 64) {
+        if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = amax;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < THREADS / 64; ++i) amax = fmaxf(amax, sh[i]);
+    }
+    // ceil(log2(amax / 448)): 448 = 1.75 * 2^8, so the exponent goes up by one
+    // where the fraction is above .75
+    int e = (int)((__builtin_bit_cast(uint32_t, amax) + 0x1fffffu) >> 23) - 127 - 8;
+    e = e < kKvMinExp ? kKvMinExp : e > kKvMaxExp ? kKvMaxExp : e;
+    if (a > 0) {
+        // earlier tokens: keep their scale, or shift their codes to the new one
+        int old = (int)*scale - 127;
+        old = old < kKvMinExp ? kKvMinExp : old > kKvMaxExp ? kKvMaxExp : old;
+        if (old >= e) {
+            e = old;
+        } else {
+            const float f = pow2f(old - e);
+            for (int i = threadIdx.x; i < a * D; i += THREADS) {
+                uint8_t *p = is_v ? codes + (size_t)(i / a) * page + i % a : codes + i;
+                *p = (uint8_t)pack_fp8x4(fp8_value(*p) * f, 0.f, 0.f, 0.f);
+            }
+        }
+    }
+    const float inv = pow2f(-e);
+    const bool top = e == kKvMaxExp;
+    if constexpr (THREADS > 64) __syncthreads();  // every thread has read the old scale
+    if (threadIdx.x == 0) *scale = (uint8_t)(e + 127);
+    for (int i = threadIdx.x; i < m * vpr; i += THREADS) {
+        const int t = i / vpr, d = (i - t * vpr) * 8;
+        const u32x4 x = *reinterpret_cast<const u32x4 *>(in + (row + t) * ld + d);
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = scaled(f16_bits_to_f32((x[j >> 1] >> (16 * (j & 1))) & 0xffffu), inv, top);
+        const u32x2 o{pack_fp8x4(f[0], f[1], f[2], f[3]), pack_fp8x4(f[4], f[5], f[6], f[7])};
+        if (!is_v) {
+            *reinterpret_cast<u32x2 *>(codes + (size_t)(a + t) * D + d) = o;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                codes[(size_t)(d + j) * page + a + t] = (uint8_t)(o[j >> 2] >> (8 * (j & 3)));
+        }
+    }
+}
+
+}  // namespace
+
+hipError_t launch_kv_append(const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv, const CacheArgs &c,
+                            const SeqArgs &s, hipStream_t stream) {
+    if (!s.rows) {
+        // single tokens: one wave per (sequence, head)
+        kv_append_kernel<64><<<dim3((unsigned)s.B, (unsigned)c.heads, 2), dim3(64), 0, stream>>>(k, ldk, v, ldv, c, s);
+    } else {
+        const unsigned ids = (unsigned)((s.T >> c.page_shift) + 2 * (int64_t)s.B);
+        kv_append_kernel<256><<<dim3(ids, (unsigned)c.heads, 2), dim3(256), 0, stream>>>(k, ldk, v, ldv, c, s);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace w4a16
