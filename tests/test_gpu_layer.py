@@ -503,7 +503,7 @@ def test_attention_stale_codes_beyond_fp16(counts):
     c = empty_cache(4, H, page, D, g)
     c["k"][:], c["v"][:], c["k_scale"][:], c["v_scale"][:] = 0x7E, 0xFE, 135, 135
     k, v = synth.activations(g, n, H * D), synth.activations(g, n, H * D)
-    v[::10] = 65504
+    v[::8] = 65504
     lo.kv_append(k, v, c, table, [n], [0, n])
     assert (c["v_scale"][[2, 0, 1]] == 135).all()
     q = synth.activations(g, counts[0], 2 * H * D)
