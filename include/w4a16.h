@@ -346,10 +346,16 @@ int w4a16_quant_fp8(int act, const uint16_t *x, int64_t ldx, int64_t M, int64_t 
  * NaN codes and non-finite scales propagate to the outputs they enter.
  * Errors: INVALID_ARG for NULL pointers, sizes <= 0 (M < 0), overlap;
  * UNSUPPORTED for K % 16 != 0, pointers that are not 16-byte aligned (scales:
- * 4-byte), M > 2^20, K or N > 2^26; HIP on launch failure.
+ * 4-byte), M > 2^20, K or N > 2^26, M * N past one launch (2^36); HIP on
+ * launch failure.
  */
 int w4a16_gemm_fp8(const uint8_t *a, const float *a_scales, const uint8_t *b, const float *b_scales, int64_t M,
                    int64_t K, int64_t N, uint16_t *out, hipStream_t stream);
+
+/* The workgroup tile (rows x cols of out) and the number of wave groups that
+ * divide K which w4a16_gemm_fp8 takes for a size (host-only, no HIP calls).
+ * Returns what w4a16_gemm_fp8 would return for the sizes alone. */
+int w4a16_gemm_fp8_plan(int64_t M, int64_t K, int64_t N, int32_t *rows, int32_t *cols, int32_t *groups);
 
 /*
  * A paged key/value cache in 8 bits (host struct; pointers are device).  A

@@ -174,6 +174,11 @@ def test_quant_special_values():
 GEMMS = [(1, 16, 1), (1, 112, 3), (2, 128, 16), (5, 144, 17), (16, 256, 100), (17, 1024, 128), (33, 2064, 130),
          (64, 384, 1000), (65, 512, 256), (130, 640, 264), (3, 12800, 128), (1, 4096, 6144), (128, 256, 384),
          (200, 1040, 520), (257, 144, 777), (300, 2048, 1024), (512, 128, 512), (1, 128, 40000), (1000, 400, 72)]
+# one size at least for every tile shape, with ragged rows, columns and blocks (their outputs are sampled)
+SHAPES = {(16, 16, 8): (5, 4112, 4090), (32, 32, 4): (30, 2000, 3000), (32, 64, 2): (60, 1424, 6100), (32, 64, 1): (1, 272, 18000),
+          (64, 64, 2): (125, 1296, 6000), (64, 64, 1): (97, 272, 12000), (64, 128, 2): (190, 2064, 6001),
+          (64, 128, 1): (190, 272, 13000), (128, 128, 2): (100, 1936, 18000),
+          (128, 256, 1): (1000, 1680, 5000), (256, 256, 1): (2010, 1168, 6100)}
 
 
 def gemm_inputs(M, K, N, seed):
@@ -199,6 +204,30 @@ def test_gemm_fp8(M, K, N):
     out = host(w4.w4a16_gemm_fp8(*args))
     check(out, want, gemm_bound(want, err), "gemm_fp8")
     assert np.array_equal(out, host(w4.w4a16_gemm_fp8(*args))), "not the same twice"
+
+
+@pytest.mark.parametrize("shape", list(SHAPES))
+def test_gemm_fp8_tile_shapes(shape):
+    """Every tile shape: some rows in full (the first, the last and some between), against the oracle and, exactly, with
+    integers whose sums are exact."""
+    M, K, N = SHAPES[shape]
+    assert w4.w4a16_gemm_fp8_plan(M, K, N) == shape
+    note("gemm_fp8 %s M=%d K=%d N=%d" % (shape, M, K, N))
+    a, sa, b, sb = gemm_inputs(M, K, N, M + K + N)
+    rows = np.unique(np.linspace(0, M - 1, 9).astype(int))
+    bd, sbd = codes_dev(b), dev(sb)
+    out = host(w4.w4a16_gemm_fp8(codes_dev(a), dev(sa), bd, sbd))
+    want, err = lo.gemm_fp8(a[rows], sa[rows], b, sb)
+    check(out[rows], want, gemm_bound(want, err), "rows")
+    g = synth.rng(5)
+    ai, bi = g.integers(-2, 3, (M, K)), g.integers(-2, 3, (N, K))
+    sa, sb = (2.0 ** g.integers(-1, 2, s.shape).astype(np.float32) for s in (sa, sb))
+    out = host(w4.w4a16_gemm_fp8(codes_dev(lo.fp8_codes(ai.astype(np.float64))), dev(sa),
+                                 codes_dev(lo.fp8_codes(bi.astype(np.float64))), dev(sb)))
+    fa = torch.from_numpy((ai * lo.spread(sa.astype(np.float64), K))).cuda()
+    fb = torch.from_numpy((bi * lo.spread(np.repeat(sb.astype(np.float64), 128, 0)[:N], K))).cuda()
+    # sums of at most 2000 quarters of integers up to 16 are exact in fp32, their fp16 roundings compared bit for bit
+    assert np.array_equal(out, host((fa @ fb.t().contiguous()).half()))
 
 
 @pytest.mark.parametrize("M,K,N", [(1, 272, 40), (20, 272, 40), (300, 272, 300)])

@@ -30,7 +30,8 @@ __all__ = [
     "w4a16_decode_workspace_bytes", "w4a16_gemm_glue", "w4a16_gemm_glue_workspace_bytes", "w4a16_rownorm",
     "w4a16_gemm_plan", "w4a16_set_tuning", "w4a16_release", "Linear", "STATUS",
     "GLUE_NONE", "GLUE_RMSNORM", "GLUE_SWIGLU",
-    "w4a16_add_rmsnorm", "w4a16_add_rmsnorm_fp8", "w4a16_quant_fp8", "w4a16_gemm_fp8", "w4a16_kv_cache",
+    "w4a16_add_rmsnorm", "w4a16_add_rmsnorm_fp8", "w4a16_quant_fp8", "w4a16_gemm_fp8",
+    "w4a16_gemm_fp8_plan", "w4a16_kv_cache",
     "w4a16_kv_append", "w4a16_attention", "w4a16_attention_workspace_bytes", "w4a16_decode_step_kv",
     "w4a16_decode_kv_workspace_bytes", "KVCache", "ACT_NONE", "ACT_SWIGLU",
 ]
@@ -112,6 +113,8 @@ def lib() -> ctypes.CDLL:
     L.w4a16_quant_fp8.argtypes = [ctypes.c_int, P, I64, I64, I64, P, P, P]
     L.w4a16_gemm_fp8.restype = ctypes.c_int
     L.w4a16_gemm_fp8.argtypes = [P, P, P, P, I64, I64, I64, P, P]
+    L.w4a16_gemm_fp8_plan.restype = ctypes.c_int
+    L.w4a16_gemm_fp8_plan.argtypes = [I64, I64, I64] + [ctypes.POINTER(ctypes.c_int32)] * 3
     L.w4a16_kv_append.restype = ctypes.c_int
     L.w4a16_kv_append.argtypes = [P, I64, P, I64, P, P, I64, P, P, I64, I64, P]
     L.w4a16_attention_workspace_bytes.restype = SZ
@@ -502,6 +505,14 @@ def w4a16_gemm_fp8(a, a_scales, b, b_scales, out=None):
     _launch(a.device, lib().w4a16_gemm_fp8, a.data_ptr(), a_scales.data_ptr(), b.data_ptr(), b_scales.data_ptr(), M, K,
             N, out.data_ptr())
     return out
+
+
+def w4a16_gemm_fp8_plan(M, K, N):
+    """(rows, cols, groups): the workgroup tile and the wave groups dividing K that
+    w4a16_gemm_fp8 takes for a size."""
+    r, c, g = ctypes.c_int32(), ctypes.c_int32(), ctypes.c_int32()
+    _check(lib().w4a16_gemm_fp8_plan(M, K, N, ctypes.byref(r), ctypes.byref(c), ctypes.byref(g)))
+    return r.value, c.value, g.value
 
 
 def w4a16_kv_cache(pages, heads, page, dim, device="cuda"):

@@ -107,6 +107,17 @@ int attention_plan(int64_t heads, const CacheArgs &c, int64_t max_pages, int64_t
     return W4A16_OK;
 }
 
+int check_gemm_fp8(int64_t M, int64_t K, int64_t N) {
+    if (M < 0 || K <= 0 || N <= 0) return fail(W4A16_ERR_INVALID_ARG, "M must be >= 0, K and N positive");
+    if (K % 16 != 0) return fail(W4A16_ERR_UNSUPPORTED, "K must be a multiple of 16");
+    if (M > kMaxRows || K > ((int64_t)1 << 26) || N > ((int64_t)1 << 26))
+        return fail(W4A16_ERR_UNSUPPORTED, "M above 2^20, or K or N above 2^26");
+    // workgroups of the smallest tiles, and of the row kernel
+    if (cdiv(M, 16) * cdiv(N, 16) > kMaxGrid * 16 || cdiv(N, 16) > kMaxGrid)
+        return fail(W4A16_ERR_UNSUPPORTED, "M * N too large for one launch");
+    return W4A16_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -164,12 +175,10 @@ int w4a16_quant_fp8(int act, const uint16_t *x, int64_t ldx, int64_t M, int64_t 
 int w4a16_gemm_fp8(const uint8_t *a, const float *a_scales, const uint8_t *b, const float *b_scales, int64_t M,
                    int64_t K, int64_t N, uint16_t *out, hipStream_t stream) {
     if (!b || !b_scales) return fail(W4A16_ERR_INVALID_ARG, "b and b_scales must be non-NULL");
-    if (M < 0 || K <= 0 || N <= 0) return fail(W4A16_ERR_INVALID_ARG, "M must be >= 0, K and N positive");
+    int rc = check_gemm_fp8(M, K, N);
+    if (rc != W4A16_OK) return rc;
     if (M == 0) return ok();
     if (!a || !a_scales || !out) return fail(W4A16_ERR_INVALID_ARG, "a, a_scales and out must be non-NULL when M > 0");
-    if (K % 16 != 0) return fail(W4A16_ERR_UNSUPPORTED, "K must be a multiple of 16");
-    if (M > kMaxRows || K > ((int64_t)1 << 26) || N > ((int64_t)1 << 26))
-        return fail(W4A16_ERR_UNSUPPORTED, "M above 2^20, or K or N above 2^26");
     if (!aligned16(a) || !aligned16(b) || !aligned16(out) || !aligned4(a_scales) || !aligned4(b_scales))
         return fail(W4A16_ERR_UNSUPPORTED, "a, b and out must be 16-byte aligned, the scales 4-byte aligned");
     const int64_t kb = cdiv(K, kFp8Block);
@@ -178,6 +187,17 @@ int w4a16_gemm_fp8(const uint8_t *a, const float *a_scales, const uint8_t *b, co
                Range{b_scales, (size_t)cdiv(N, kFp8Block) * kb * 4}}))
         return fail(W4A16_ERR_INVALID_ARG, "out overlaps an input");
     return hip_status(launch_gemm_fp8(a, a_scales, b, b_scales, M, K, N, out, stream), "8-bit GEMM");
+}
+
+int w4a16_gemm_fp8_plan(int64_t M, int64_t K, int64_t N, int32_t *rows, int32_t *cols, int32_t *groups) {
+    int rc = check_gemm_fp8(M, K, N);
+    if (rc != W4A16_OK) return rc;
+    int32_t r, c, g;
+    gemm_fp8_plan(std::max<int64_t>(M, 1), K, N, &r, &c, &g);
+    if (rows) *rows = r;
+    if (cols) *cols = c;
+    if (groups) *groups = g;
+    return ok();
 }
 
 int w4a16_kv_append(const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv, const w4a16_kv_cache *cache,

@@ -48,6 +48,9 @@ hipError_t launch_quant_fp8(bool swiglu, const uint16_t *x, int64_t ldx, int64_t
                             float *scales, hipStream_t stream);
 hipError_t launch_gemm_fp8(const uint8_t *a, const float *sa, const uint8_t *b, const float *sb, int64_t M, int64_t K,
                            int64_t N, uint16_t *out, hipStream_t stream);
+// The workgroup tile (rows x columns) and the groups K is divided among that a
+// size takes.
+void gemm_fp8_plan(int64_t M, int64_t K, int64_t N, int32_t *rows, int32_t *cols, int32_t *groups);
 hipError_t launch_kv_append(const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv, const CacheArgs &c,
                             const SeqArgs &s, hipStream_t stream);
 
