@@ -119,169 +119,130 @@ __device__ __forceinline__ float inverse(float l, int pos) {
     return l != 0.f ? 1.0f / l : pos < 0 ? 0.f : __builtin_nanf("");
 }
 
-// NT 16-column tiles per wave.  SHARED: the workgroup's four waves hold the
-// same columns and take chunks in turn; otherwise wave w holds columns
-// [w * 16 NT, (w + 1) * 16 NT) of the tile and walks all of its chunks.
-template <int D, int NT, bool SHARED>
-__global__ __launch_bounds__(256) void attention_kernel(Params p) {
-    constexpr int KD = D / 64;   // 16-byte key loads per lane and 16-token tile
-    constexpr int DT = D / 16;   // output tiles along dim
-    __shared__ __align__(16) float lds_o[SHARED ? 4 * 16 * D : 4];
-    __shared__ float lds_ml[SHARED ? 4 * 16 * 2 : 2];
+// Pages of a column tile's tokens.  lookup() gives the page of the 16-token
+// block x of chunk c: -1 where the block lies behind the tile's tokens (nothing
+// there is used), -2 where the table's entry is out of range; slot() a page's
+// place among the cache's (page, head) pairs, page 0 for either.
+struct Pages {
+    const int32_t *table;
+    int64_t pages;
+    int heads, kvh, shift, hi;
+    __device__ __forceinline__ Pages(const Params &p, const Tile &t, int kvh_)
+        : table(p.s.table + (int64_t)t.b * p.s.max_pages), pages(p.c.pages), heads(p.c.heads), kvh(kvh_),
+          shift(p.c.page_shift), hi(t.hi) {}
+    __device__ __forceinline__ int lookup(int c, int x) const {
+        const int tok = c * kChunk + 16 * x;
+        if (tok >= hi) return -1;
+        const int id = table[tok >> shift];
+        return id < 0 || id >= pages ? -2 : id;
+    }
+    __device__ __forceinline__ size_t slot(int page) const { return (size_t)(page < 0 ? 0 : page) * heads + kvh; }
+    // byte offset of block x of chunk c within its page's rows of D (keys)
+    __device__ __forceinline__ int within(int c, int x) const { return (c * kChunk + 16 * x) & ((1 << shift) - 1); }
+};
 
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int col = lane & 15, g = lane >> 4, kx = col >> 2;
-    const int kvh = blockIdx.x % p.c.heads;
-    const int rest = blockIdx.x / p.c.heads;
-    const int split = rest % p.splits;
-    const int tile = p.tiles - 1 - rest / p.splits;
-    const Tile t = make_tile(p, tile);
-    if (t.c0 >= t.ncols || (split > 0 && split >= t.active)) return;
+// NT tiles of 16 columns held by one wave: queries, running maxima, the sums of
+// the weights (one more row of O, from values of one) and O, all of it fp32.
+template <int D, int NT>
+struct Columns {
+    static constexpr int KD = D / 64;  // 16-byte key pieces per lane and 16-token tile
+    static constexpr int DT = D / 16;  // output tiles along dim
 
-    // this wave's columns and chunks
-    const int wc0 = t.c0 + (SHARED ? 0 : wave * 16 * NT);
-    int clo = t.split0 + split * p.quota;
-    int chi = (t.hi + kChunk - 1) / kChunk;
-    chi = chi < clo + p.quota ? chi : clo + p.quota;
-    if (t.hi <= t.lo) chi = clo;
-    int pos[NT];
+    int pos[NT];   // position of this lane's column
     bool live[NT];
-    int wcl = wc0 + 16 * NT < t.ncols ? wc0 + 16 * NT : t.ncols;  // end of the valid ones
-    if (!SHARED) {
-        if (wc0 >= t.ncols) return;
-        const int64_t whi = (int64_t)t.first + (wcl - 1) / p.group + 1;
-        const int wch = whi <= 0 ? 0 : (int)((whi + kChunk - 1) / kChunk);
-        chi = chi < wch ? chi : wch;
-        if (p.window) {
-            const int64_t wlo = (int64_t)t.first + wc0 / p.group - p.window + 1;
-            const int wcl0 = wlo <= 0 ? 0 : (int)(wlo / kChunk);
-            clo = clo > wcl0 ? clo : wcl0;
+    int pos_min, pos_max;
+    f16x8 qf[NT][2 * KD];
+    f32x4 o[NT][DT], l[NT];
+    float mx[NT];  // of scores before their scale
+    float scale, lazy;
+    int window, hi;
+
+    // Columns wc0 .. wc0 + 16 NT of the tile's sequence.  Lane (c, g) holds
+    // dims 64m + 16g .. + 15 of column c's query, the order in which keys come.
+    __device__ __forceinline__ void init(const Params &p, const Tile &t, int kvh, int wc0) {
+        const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+        // A negative scale goes into the sign of q, so that the largest product
+        // has the largest score.  (The floor keeps a scale of zero from meeting
+        // the infinities of masked scores; products are below 2^40, so nothing
+        // else sees it.)
+        scale = fmaxf(__builtin_fabsf(p.scale), 0x1p-100f);
+        lazy = kLazy / scale;
+        window = p.window;
+        hi = t.hi;
+        const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
+        const int end = wc0 + 16 * NT < t.ncols ? wc0 + 16 * NT : t.ncols;
+        pos_min = t.first + wc0 / p.group;
+        pos_max = t.first + (end - 1) / p.group;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int cc = wc0 + 16 * n + col;
+            live[n] = cc < t.ncols;
+            const int i = live[n] ? cc / p.group : 0, h = live[n] ? cc - i * p.group : 0;
+            pos[n] = live[n] ? t.first + i : pos_max;
+            const uint16_t *src = p.q + (int64_t)(t.r0 + i) * p.ldq + (int64_t)(kvh * p.group + h) * D + 16 * g;
+#pragma unroll
+            for (int m = 0; m < KD; ++m)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    u32x4 v{0u, 0u, 0u, 0u};
+                    if (live[n]) v = *reinterpret_cast<const u32x4 *>(src + 64 * m + 8 * x);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[j] ^= flip;
+                    qf[n][2 * m + x] = __builtin_bit_cast(f16x8, v);
+                }
+            mx[n] = -__builtin_inff();
+            l[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int d = 0; d < DT; ++d) o[n][d] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
     }
-    const int pos_min = t.first + wc0 / p.group, pos_max = t.first + (wcl - 1) / p.group;
 
-    // Q fragments: lane (c, g) holds dims 64m + 16g .. + 15 of column c, the
-    // order in which it reads keys.
-    f16x8 qf[NT][2 * KD];
+    // Scores of chunk c: S^T, before the scale.  key(x, m): this lane's piece m
+    // of its token of tile x.
+    template <typename Key>
+    __device__ __forceinline__ void scores(f32x4 (&sc)[NT][4], Key key, float fk) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int cc = wc0 + 16 * n + col;
-        live[n] = cc < t.ncols;
-        const int i = live[n] ? cc / p.group : 0, h = live[n] ? cc - i * p.group : 0;
-        pos[n] = live[n] ? t.first + i : pos_max;
-        const uint16_t *src = p.q + (int64_t)(t.r0 + i) * p.ldq + (int64_t)(kvh * p.group + h) * D + 16 * g;
+        for (int x = 0; x < 4; ++x) {
 #pragma unroll
-        for (int m = 0; m < KD; ++m)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                u32x4 v{0u, 0u, 0u, 0u};
-                if (live[n]) v = *reinterpret_cast<const u32x4 *>(src + 64 * m + 8 * x);
-                qf[n][2 * m + x] = __builtin_bit_cast(f16x8, v);
-            }
-    }
-
-    f32x4 o[NT][DT];
-    float mx[NT], sum[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        mx[n] = -__builtin_inff();
-        sum[n] = 0.f;
-#pragma unroll
-        for (int d = 0; d < DT; ++d) o[n][d] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
-
-    const size_t page_bytes = (size_t)D << p.c.page_shift;
-    const int page_mask = (1 << p.c.page_shift) - 1;
-    const int32_t *table = p.s.table + (int64_t)t.b * p.s.max_pages;
-    // Page of the 16-token block x of chunk c: -1 where the block lies behind
-    // the tile's tokens (nothing there is read), -2 where the table's entry is
-    // out of range.
-    auto page_of = [&](int c, int x) {
-        const int tok = c * kChunk + 16 * x;
-        if (tok >= t.hi) return -1;
-        const int id = table[tok >> p.c.page_shift];
-        return id < 0 || id >= p.c.pages ? -2 : id;
-    };
-    for (int c = SHARED ? clo + wave : clo; c < chi; c += SHARED ? 4 : 1) {
-        const int pk = page_of(c, kx), pv = page_of(c, g);
-        const size_t sk = (size_t)(pk < 0 ? 0 : pk) * p.c.heads + kvh, sv = (size_t)(pv < 0 ? 0 : pv) * p.c.heads + kvh;
-        const int offk = (c * kChunk + 16 * kx) & page_mask, offv = (c * kChunk + 16 * g) & page_mask;
-        const uint8_t *kp = p.c.k + sk * page_bytes + (size_t)(offk + (col & 3)) * D + 16 * g;
-        const uint8_t *vp = p.c.v + sv * page_bytes + ((size_t)col << p.c.page_shift) + offv;
-        const float fk = scale_of(p.c.k_scale[sk]), fv = scale_of(p.c.v_scale[sv]);
-        u32x4 kr[4][KD], vr[DT];
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-#pragma unroll
-            for (int m = 0; m < KD; ++m) kr[x][m] = *reinterpret_cast<const u32x4 *>(kp + (size_t)(4 * x) * D + 64 * m);
-#pragma unroll
-        for (int d = 0; d < DT; ++d)
-            vr[d] = *reinterpret_cast<const u32x4 *>(vp + ((size_t)(16 * d) << p.c.page_shift));
-
-        f32x4 sc[NT][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) sc[n][x] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
+            for (int n = 0; n < NT; ++n) sc[n][x] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int m = 0; m < KD; ++m) {
-                const f16x8 a0 = dequant8(kr[x][m][0], kr[x][m][1], fk), a1 = dequant8(kr[x][m][2], kr[x][m][3], fk);
+                const u32x4 k = key(x, m);
+                const f16x8 a0 = dequant8(k[0], k[1], fk), a1 = dequant8(k[2], k[3], fk);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     sc[n][x] = mfma16(a0, qf[n][2 * m], sc[n][x]);
                     sc[n][x] = mfma16(a1, qf[n][2 * m + 1], sc[n][x]);
                 }
             }
+        }
+    }
+
+    // Whether some column does not see all of chunk c.
+    __device__ __forceinline__ bool partial(int c) const {
+        const int lo = c * kChunk;
+        return lo + kChunk - 1 > pos_min || (window && lo <= pos_max - window);
+    }
+
+    // Masked scores become -inf whatever they hold; a page out of range (of
+    // this lane's tokens) makes the ones that are seen NaN.
+    __device__ __forceinline__ void mask(f32x4 (&sc)[NT][4], int c, bool bad) const {
+        const int tok0 = c * kChunk + 16 * ((threadIdx.x & 63) >> 4);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int x = 0; x < 4; ++x)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sc[n][x][i] *= p.scale;
-
-        // Chunks that some column does not see whole: masked scores are set to
-        // -inf whatever they hold, a page out of range makes them NaN, and NaN
-        // codes among the values are taken out, to be put back only for the
-        // columns that see them.
-        const int c_lo = c * kChunk, c_hi = c_lo + kChunk;
-        const bool partial = c_hi - 1 > pos_min || (p.window && c_lo <= pos_max - p.window);
-        bool odd = false;  // some value code was NaN
-        u32x4 vnan[DT];
-        if (partial || __any(pk == -2 || pv == -2)) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int tok = c_lo + 16 * g + 4 * x + i;
-                        const bool seen = tok <= pos[n] && (!p.window || tok > pos[n] - p.window) && tok < t.hi;
-                        sc[n][x][i] = !seen ? -__builtin_inff() : pv == -2 ? __builtin_nanf("") : sc[n][x][i];
-                    }
-            // tokens past the tile's last (or on a page out of range): zero codes,
-            // whatever lies there (old codes may even overflow at the new scale)
-            const int left = pv < 0 ? 0 : t.hi - (c_lo + 16 * g);
-            uint32_t any = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int n = left - 4 * j;
-                const uint32_t keep = n >= 4 ? 0xffffffffu : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
-#pragma unroll
-                for (int d = 0; d < DT; ++d) {
-                    vr[d][j] &= keep;
-                    const uint32_t bad = nan_bits(vr[d][j]);
-                    any |= bad;
-                    vnan[d][j] = (bad >> 7) * 0x38u;  // 1.0 where the code was NaN
-                    vr[d][j] &= ~((bad >> 7) * 0xffu);
+                for (int i = 0; i < 4; ++i) {
+                    const int tok = tok0 + 4 * x + i;
+                    const bool seen = tok <= pos[n] && (!window || tok > pos[n] - window) && tok < hi;
+                    sc[n][x][i] = !seen ? -__builtin_inff() : bad ? __builtin_nanf("") : sc[n][x][i];
                 }
-            }
-            odd = __any(any != 0);
-        }
+    }
 
-        // Running maxima: raised when a score passes them by kLazy.
-        f16x8 pf[NT][2], seen_f[NT][2];
+    // Weights of a chunk, rounded to fp16.  The running maxima are raised when
+    // a score passes them by kLazy after its scale.
+    __device__ __forceinline__ void weights(const f32x4 (&sc)[NT][4], f16x8 (&pf)[NT][2]) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             float top = -__builtin_inff();
@@ -289,132 +250,381 @@ __global__ __launch_bounds__(256) void attention_kernel(Params p) {
             for (int x = 0; x < 4; ++x)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[n][x][i]);
-            if (__any(top > mx[n] + kLazy)) {
+            if (__any(top > mx[n] + lazy)) {
                 top = fmaxf(top, __shfl_xor(top, 16));
                 top = fmaxf(top, __shfl_xor(top, 32));
                 const float m = fmaxf(mx[n], top);
-                const float f = m == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(mx[n] - m);
+                const float f = m == mx[n] ? 1.0f : __builtin_amdgcn_exp2f((mx[n] - m) * scale);
                 mx[n] = m;
-                sum[n] *= f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) l[n][i] *= f;
 #pragma unroll
                 for (int d = 0; d < DT; ++d)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o[n][d][i] *= f;
             }
-            const float base = mx[n] == -__builtin_inff() ? 0.f : mx[n];
+            const float base = mx[n] == -__builtin_inff() ? 0.f : mx[n] * scale;
 #pragma unroll
             for (int x = 0; x < 4; ++x)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float e = __builtin_amdgcn_exp2f(sc[n][x][i] - base);
-                    sum[n] += e;
-                    pf[n][x >> 1][4 * (x & 1) + i] = (f16)e;
-                    if (odd) seen_f[n][x >> 1][4 * (x & 1) + i] = sc[n][x][i] == -__builtin_inff() ? (f16)0 : (f16)1;
-                }
+                for (int i = 0; i < 4; ++i)
+                    pf[n][x >> 1][4 * (x & 1) + i] =
+                        (f16)__builtin_amdgcn_exp2f(__builtin_fmaf(sc[n][x][i], scale, -base));
+        }
+    }
+
+    // O += V^T P.  value(d): this lane's 16 codes of output tile d.  CLEAN: every
+    // column sees the whole chunk, and NaN among the values is every column's.
+    // Otherwise codes of tokens past the tile's last (or on a page out of
+    // range: left 0) count as zero, whatever lies there (old codes may even
+    // overflow at the new scale), and NaN codes are taken out and put back only
+    // for the columns that see them: those for which a product of ones counts.
+    template <bool CLEAN, typename Value>
+    __device__ __forceinline__ void values(const f32x4 (&sc)[NT][4], const f16x8 (&pf)[NT][2], Value value, float fv,
+                                           int left) {
+        f16x8 ones;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ones[j] = (f16)1;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            l[n] = mfma16(ones, pf[n][0], l[n]);
+            l[n] = mfma16(ones, pf[n][1], l[n]);
         }
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
-            const f16x8 a0 = dequant8(vr[d][0], vr[d][1], fv), a1 = dequant8(vr[d][2], vr[d][3], fv);
+            u32x4 v = value(d);
+            if constexpr (!CLEAN) {
+                uint32_t any = 0, count[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int n = left - 4 * j;
+                    v[j] &= n >= 4 ? 0xffffffffu : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
+                    const uint32_t nan = nan_bits(v[j]) >> 7;
+                    any |= nan;
+                    count[j] = nan * 0x38u;  // e4m3 1.0
+                    v[j] &= ~(nan * 0xffu);
+                }
+                if (__any(any != 0)) {
+                    const f16x8 a0 = dequant8(count[0], count[1], 1.f), a1 = dequant8(count[2], count[3], 1.f);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        f16x8 s0, s1;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            s0[j] = sc[n][j >> 2][j & 3] == -__builtin_inff() ? (f16)0 : (f16)1;
+                            s1[j] = sc[n][2 + (j >> 2)][j & 3] == -__builtin_inff() ? (f16)0 : (f16)1;
+                        }
+                        f32x4 z{0.f, 0.f, 0.f, 0.f};
+                        z = mfma16(a0, s0, z);
+                        z = mfma16(a1, s1, z);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (z[i] > 0.f) o[n][d][i] = __builtin_nanf("");
+                    }
+                }
+            }
+            const f16x8 a0 = dequant8(v[0], v[1], fv), a1 = dequant8(v[2], v[3], fv);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 o[n][d] = mfma16(a0, pf[n][0], o[n][d]);
                 o[n][d] = mfma16(a1, pf[n][1], o[n][d]);
             }
         }
-        if (odd) {
-#pragma unroll
-            for (int d = 0; d < DT; ++d) {
-                const f16x8 a0 = dequant8(vnan[d][0], vnan[d][1], 1.f), a1 = dequant8(vnan[d][2], vnan[d][3], 1.f);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    f32x4 z{0.f, 0.f, 0.f, 0.f};
-                    z = mfma16(a0, seen_f[n][0], z);
-                    z = mfma16(a1, seen_f[n][1], z);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (z[i] > 0.f) o[n][d][i] = __builtin_nanf("");
-                }
-            }
-        }
-    }
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        sum[n] += __shfl_xor(sum[n], 16);
-        sum[n] += __shfl_xor(sum[n], 32);
-        if (pos[n] >= t.cap) sum[n] = __builtin_nanf("");  // longer than its table: loud
     }
 
-    const int64_t slot = ((int64_t)tile * p.c.heads + kvh) * p.splits + split;
-    if constexpr (!SHARED) {
+    // Maximum in powers of two, and sum, of this lane's column.
+    __device__ __forceinline__ float max2(int n) const { return mx[n] * scale; }
+    __device__ __forceinline__ float total(int n, int cap) const {
+        return pos[n] >= cap ? __builtin_nanf("") : l[n][0];  // longer than its table: loud
+    }
+};
+
+__device__ __forceinline__ u32x2 pack4(const f32x4 &v, float f) {
+    u32x2 w;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int cc = wc0 + 16 * n + col;
-            if (!live[n]) continue;
-            if (t.active <= 1) {
-                const int i = cc / p.group, h = cc - i * p.group;
-                uint16_t *dst = p.out + ((int64_t)(t.r0 + i) * p.heads + kvh * p.group + h) * D + 4 * g;
-                const float f = inverse(sum[n], t.first + i);
+    for (int j = 0; j < 2; ++j)
+        w[j] = (uint32_t)f32_to_f16_bits(v[2 * j] * f) | ((uint32_t)f32_to_f16_bits(v[2 * j + 1] * f) << 16);
+    return w;
+}
+
+// This workgroup's place in the grid: key/value heads in turn (an XCD then
+// keeps to the same heads), pieces of a tile, and tiles from the last, which
+// see the most tokens.
+struct Place {
+    int kvh, split, tile;
+    __device__ __forceinline__ explicit Place(const Params &p) {
+        kvh = blockIdx.x % p.c.heads;
+        const int rest = blockIdx.x / p.c.heads;
+        split = rest % p.splits;
+        tile = p.tiles - 1 - rest / p.splits;
+    }
+    __device__ __forceinline__ int64_t slot(const Params &p) const {
+        return ((int64_t)tile * p.c.heads + kvh) * p.splits + split;
+    }
+};
+
+// Few columns (single tokens): the workgroup's four waves hold the same 16
+// columns and take chunks in turn, keys and values straight from memory into
+// registers.  Bound by reading the cache.  The loop is pipelined: a chunk's
+// keys are requested when those of the chunk before have been multiplied, its
+// values when those of the chunk before have; its pages are looked up one
+// chunk earlier still.
+template <int D>
+__global__ __launch_bounds__(256, (D == 64 ? 3 : D == 128 ? 2 : 1)) void attention_token_kernel(Params p) {
+    constexpr int KD = D / 64, DT = D / 16;
+    __shared__ __align__(16) float lds_o[4 * 16 * D];
+    __shared__ float lds_ml[4 * 16 * 2];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, g = lane >> 4, kx = col >> 2;
+    const Place at(p);
+    const Tile t = make_tile(p, at.tile);
+    if (t.c0 >= t.ncols || (at.split > 0 && at.split >= t.active)) return;
+    const int clo = t.split0 + at.split * p.quota;
+    int chi = t.hi > t.lo ? (t.hi + kChunk - 1) / kChunk : clo;
+    chi = chi < clo + p.quota ? chi : clo + p.quota;
+
+    Columns<D, 1> cs;
+    cs.init(p, t, at.kvh, t.c0);
+    const Pages pages(p, t, at.kvh);
+    const size_t page_bytes = (size_t)D << p.c.page_shift;
+    u32x4 kr[4][KD], vr[DT];
+    int pk = -1, pv = -1;     // pages of the chunk whose keys / values are in hand
+    uint32_t bk = 0, bv = 0;  // their scale bytes
+    auto load_keys = [&](int c, int page) __attribute__((always_inline)) {
+        const size_t sk = pages.slot(page);
+        const uint8_t *kp = p.c.k + sk * page_bytes + (size_t)(pages.within(c, kx) + (col & 3)) * D + 16 * g;
+        bk = p.c.k_scale[sk];
 #pragma unroll
-                for (int d = 0; d < DT; ++d) {
-                    u32x2 w;
+        for (int x = 0; x < 4; ++x)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        w[j] = (uint32_t)f32_to_f16_bits(o[n][d][2 * j] * f) |
-                               ((uint32_t)f32_to_f16_bits(o[n][d][2 * j + 1] * f) << 16);
-                    *reinterpret_cast<u32x2 *>(dst + 16 * d) = w;
-                }
-            } else {
-                float *dst = p.part + (slot * p.cols + (cc - t.c0)) * D + 4 * g;
+            for (int m = 0; m < KD; ++m) kr[x][m] = *reinterpret_cast<const u32x4 *>(kp + 4 * x * D + 64 * m);
+    };
+    auto load_values = [&](int c, int page) __attribute__((always_inline)) {
+        const size_t sv = pages.slot(page);
+        const uint8_t *vp = p.c.v + sv * page_bytes + ((size_t)col << p.c.page_shift) + pages.within(c, g);
+        bv = p.c.v_scale[sv];
 #pragma unroll
-                for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4 *>(dst + 16 * d) = o[n][d];
-                if (g == 0) {
-                    p.ml[(slot * p.cols + (cc - t.c0)) * 2] = mx[n];
-                    p.ml[(slot * p.cols + (cc - t.c0)) * 2 + 1] = sum[n];
-                }
+        for (int d = 0; d < DT; ++d) vr[d] = *reinterpret_cast<const u32x4 *>(vp + ((size_t)(16 * d) << p.c.page_shift));
+    };
+    int c = clo + wave, pk_next = -1, pv_next = -1;
+    if (c < chi) {
+        pk = pages.lookup(c, kx);
+        pv = pages.lookup(c, g);
+        load_keys(c, pk);
+        load_values(c, pv);
+        if (c + 4 < chi) {
+            pk_next = pages.lookup(c + 4, kx);
+            pv_next = pages.lookup(c + 4, g);
+        }
+    }
+    for (; c < chi; c += 4) {
+        const bool more = c + 4 < chi, bad = __any(pk == -2 || pv == -2);
+        f32x4 sc[1][4];
+        f16x8 pf[1][2];
+        cs.scores(sc, [&](int x, int m) { return kr[x][m]; }, scale_of((uint8_t)bk));
+        int pk_after = -1, pv_after = -1;
+        if (more) {
+            load_keys(c + 4, pk_next);
+            if (c + 8 < chi) {
+                pk_after = pages.lookup(c + 8, kx);
+                pv_after = pages.lookup(c + 8, g);
             }
         }
-    } else {
-        // The waves' pieces meet in LDS, in wave order.
+        const bool clean = !cs.partial(c) && !bad;
+        if (!clean) cs.mask(sc, c, pv == -2);
+        cs.weights(sc, pf);
+        auto value = [&](int d) { return vr[d]; };
+        if (clean) cs.template values<true>(sc, pf, value, scale_of((uint8_t)bv), 0);
+        else cs.template values<false>(sc, pf, value, scale_of((uint8_t)bv), pv < 0 ? 0 : t.hi - (c * kChunk + 16 * g));
+        if (more) load_values(c + 4, pv_next);
+        pk = pk_next;
+        pv = pv_next;
+        pk_next = pk_after;
+        pv_next = pv_after;
+    }
+
+    // The waves' pieces meet in LDS, in wave order.
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
-            *reinterpret_cast<f32x4 *>(&lds_o[(wave * 16 + col) * D + 16 * d + 4 * g]) = o[0][d];
-        if (g == 0) {
-            lds_ml[(wave * 16 + col) * 2] = mx[0];
-            lds_ml[(wave * 16 + col) * 2 + 1] = sum[0];
+    for (int d = 0; d < DT; ++d)
+        *reinterpret_cast<f32x4 *>(&lds_o[(wave * 16 + col) * D + 16 * d + 4 * g]) = cs.o[0][d];
+    if (g == 0) {
+        lds_ml[(wave * 16 + col) * 2] = cs.max2(0);
+        lds_ml[(wave * 16 + col) * 2 + 1] = cs.total(0, t.cap);
+    }
+    __syncthreads();
+    const int64_t slot = at.slot(p);
+    for (int x = threadIdx.x; x < 16 * D / 4; x += 256) {
+        const int cc = x / (D / 4), d = (x - cc * (D / 4)) * 4;
+        if (t.c0 + cc >= t.ncols) continue;
+        float m = -__builtin_inff();
+#pragma unroll
+        for (int w = 0; w < 4; ++w) m = fmaxf(m, lds_ml[(w * 16 + cc) * 2]);
+        f32x4 a{0.f, 0.f, 0.f, 0.f};
+        float l = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float mw = lds_ml[(w * 16 + cc) * 2], lw = lds_ml[(w * 16 + cc) * 2 + 1];
+            const float f = mw == -__builtin_inff() ? (lw == 0.f ? 0.f : 1.f) : __builtin_amdgcn_exp2f(mw - m);
+            const f32x4 v = *reinterpret_cast<const f32x4 *>(&lds_o[(w * 16 + cc) * D + d]);
+            l += lw * f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) a[j] = __builtin_fmaf(v[j], f, a[j]);
         }
-        __syncthreads();
-        for (int x = threadIdx.x; x < 16 * D / 4; x += 256) {
-            const int cc = x / (D / 4), d = (x - cc * (D / 4)) * 4;
-            if (t.c0 + cc >= t.ncols) continue;
-            float m = -__builtin_inff();
-#pragma unroll
-            for (int w = 0; w < 4; ++w) m = fmaxf(m, lds_ml[(w * 16 + cc) * 2]);
-            f32x4 a{0.f, 0.f, 0.f, 0.f};
-            float l = 0.f;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const float mw = lds_ml[(w * 16 + cc) * 2], lw = lds_ml[(w * 16 + cc) * 2 + 1];
-                const float f = mw == -__builtin_inff() ? (lw == 0.f ? 0.f : 1.f) : __builtin_amdgcn_exp2f(mw - m);
-                const f32x4 v = *reinterpret_cast<const f32x4 *>(&lds_o[(w * 16 + cc) * D + d]);
-                l += lw * f;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) a[j] = __builtin_fmaf(v[j], f, a[j]);
+        const int c2 = t.c0 + cc;
+        if (t.active <= 1) {
+            const int i = c2 / p.group, h = c2 - i * p.group;
+            *reinterpret_cast<u32x2 *>(p.out + ((int64_t)(t.r0 + i) * p.heads + at.kvh * p.group + h) * D + d) =
+                pack4(a, inverse(l, t.first + i));
+        } else {
+            *reinterpret_cast<f32x4 *>(p.part + (slot * p.cols + cc) * D + d) = a;
+            if (d == 0) {
+                p.ml[(slot * p.cols + cc) * 2] = m;
+                p.ml[(slot * p.cols + cc) * 2 + 1] = l;
             }
-            const int c = t.c0 + cc;
-            if (t.active <= 1) {
-                const int i = c / p.group, h = c - i * p.group;
-                const float f = inverse(l, t.first + i);
-                u32x2 w;
+        }
+    }
+}
+
+// Requests 16 bytes per lane from `src` into LDS at `to` + 16 * lane; there is
+// no register result, and the kernel waits for its loads itself.
+__device__ __forceinline__ void load_to_lds16(const uint8_t *src, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(src) : "memory");
+}
+
+// Many columns (prompts): wave w holds columns [w * 16 NT, (w + 1) * 16 NT) of
+// the workgroup's 64 NT and all four walk the tile's chunks together.  A chunk
+// (64 tokens of K and of V, as stored) is staged in LDS once for the four, in
+// two buffers, by direct loads of whole lines; each wave converts what it reads
+// to fp16 in registers.
+// LDS order: a token's keys are D / 16 pieces of 16 bytes, a dim's values four
+// (one per 16-token block); pieces are exchanged within their row so that the
+// eight lanes of a read phase, which want the same piece of different rows,
+// meet different banks.  Direct loads write in lane order, so the exchange is
+// made in the lanes' addresses.
+template <int D, int NT>
+__global__ __launch_bounds__(256, (D <= 128 ? 2 : 1)) void attention_rows_kernel(Params p) {
+    constexpr int PR = D / 16;             // pieces per token of keys
+    constexpr int LOADS = D / 64;          // direct loads per wave of keys, and of values
+    constexpr int HALF = kChunk * D;       // bytes of a chunk's keys, and of its values
+    __shared__ __align__(16) uint8_t lds[2][2 * HALF];
+    const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4, kx = col >> 2;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const Place at(p);
+    const Tile t = make_tile(p, at.tile);
+    if (t.c0 >= t.ncols || (at.split > 0 && at.split >= t.active)) return;
+    const int clo = t.split0 + at.split * p.quota;
+    int chi = t.hi > t.lo ? (t.hi + kChunk - 1) / kChunk : clo;
+    chi = chi < clo + p.quota ? chi : clo + p.quota;
+
+    // this wave's columns, and the chunks that any of them sees
+    const int wc0 = t.c0 + wave * 16 * NT;
+    const bool any_col = wc0 < t.ncols;
+    Columns<D, NT> cs;
+    cs.init(p, t, at.kvh, any_col ? wc0 : t.c0);
+    const int own_hi = !any_col || cs.pos_max < 0 ? 0 : cs.pos_max / kChunk + 1;
+    const int first_tok = p.window ? cs.pos_min - p.window + 1 : 0;
+    const int own_lo = first_tok <= 0 ? 0 : first_tok / kChunk;
+
+    const Pages pages(p, t, at.kvh);
+    const size_t page_bytes = (size_t)D << p.c.page_shift;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)&lds[0][0];
+    auto key_turn = [](int row) { return PR == 4 ? ((row >> 1) & 1) | ((row >> 3) & 2) : (row & 3) | ((row >> 2) & 4); };
+    // what this lane loads: keys of row krow (+ 1024 / D per load) of block
+    // `wave`; values of dim vdim (+ 16 per load), block vx
+    const int krow = 16 * wave + lane / PR, vdim = wave * LOADS * 16 + (lane >> 2), vx = (lane & 3) ^ ((lane >> 3) & 3);
+    auto stage = [&](int c, int page_k, int page_v) __attribute__((always_inline)) {
+        const uint32_t to = lds0 + (uint32_t)(c & 1) * (2 * HALF) + wave * LOADS * 1024;
+        const uint8_t *kp = p.c.k + pages.slot(page_k) * page_bytes + (size_t)pages.within(c, wave) * D;
+        const uint8_t *vp = p.c.v + pages.slot(page_v) * page_bytes + pages.within(c, vx);
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    w[j] = (uint32_t)f32_to_f16_bits(a[2 * j] * f) | ((uint32_t)f32_to_f16_bits(a[2 * j + 1] * f) << 16);
-                *reinterpret_cast<u32x2 *>(p.out + ((int64_t)(t.r0 + i) * p.heads + kvh * p.group + h) * D + d) = w;
-            } else {
-                *reinterpret_cast<f32x4 *>(p.part + (slot * p.cols + cc) * D + d) = a;
-                if (d == 0) {
-                    p.ml[(slot * p.cols + cc) * 2] = m;
-                    p.ml[(slot * p.cols + cc) * 2 + 1] = l;
-                }
+        for (int i = 0; i < LOADS; ++i) {
+            const int row = krow + i * (1024 / D);
+            load_to_lds16(kp + (row - 16 * wave) * D + 16 * ((lane % PR) ^ key_turn(row)), to + i * 1024);
+        }
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i)
+            load_to_lds16(vp + ((size_t)(vdim + 16 * i) << p.c.page_shift), to + HALF + i * 1024);
+    };
+
+    // what it reads: keys of row 16 (col / 4) + 4x + col % 4 (all at one turn),
+    // values of dim 16 d + col
+    int key_at[D / 64];
+#pragma unroll
+    for (int m = 0; m < D / 64; ++m) key_at[m] = (16 * kx + (col & 3)) * D + 16 * ((4 * m + g) ^ key_turn(16 * kx + (col & 3)));
+    const int value_at = col * 64 + 16 * (g ^ ((col >> 1) & 3));
+
+    // Pages and scale bytes run ahead of the chunks they belong to.
+    int pw = -1, pl = -1, pk = -1, pv = -1, pk_next = -1, pv_next = -1;
+    uint32_t bk = 0, bv = 0;
+    if (clo < chi) {
+        stage(clo, pages.lookup(clo, wave), pages.lookup(clo, vx));
+        pk = pages.lookup(clo, kx);
+        pv = pages.lookup(clo, g);
+        bk = p.c.k_scale[pages.slot(pk)];
+        bv = p.c.v_scale[pages.slot(pv)];
+        if (clo + 1 < chi) {
+            pw = pages.lookup(clo + 1, wave);
+            pl = pages.lookup(clo + 1, vx);
+            pk_next = pages.lookup(clo + 1, kx);
+            pv_next = pages.lookup(clo + 1, g);
+        }
+    }
+    for (int c = clo; c < chi; ++c) {
+        // chunk c has landed, and every wave is done with the other buffer
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        const float fk = scale_of((uint8_t)bk), fv = scale_of((uint8_t)bv);
+        const int pk_now = pk, pv_now = pv;
+        if (c + 1 < chi) {
+            stage(c + 1, pw, pl);
+            pk = pk_next;
+            pv = pv_next;
+            bk = p.c.k_scale[pages.slot(pk)];
+            bv = p.c.v_scale[pages.slot(pv)];
+            if (c + 2 < chi) {
+                pw = pages.lookup(c + 2, wave);
+                pl = pages.lookup(c + 2, vx);
+                pk_next = pages.lookup(c + 2, kx);
+                pv_next = pages.lookup(c + 2, g);
+            }
+        }
+        if (c < own_lo || c >= own_hi) continue;
+        const uint8_t *kb = &lds[c & 1][0], *vb = kb + HALF;
+        f32x4 sc[NT][4];
+        f16x8 pf[NT][2];
+        cs.scores(sc, [&](int x, int m) __attribute__((always_inline)) {
+            return *reinterpret_cast<const u32x4 *>(kb + key_at[m] + 4 * x * D);
+        }, fk);
+        const bool clean = !cs.partial(c) && !__any(pk_now == -2 || pv_now == -2);
+        if (!clean) cs.mask(sc, c, pv_now == -2);
+        cs.weights(sc, pf);
+        auto value = [&](int d) __attribute__((always_inline)) {
+            return *reinterpret_cast<const u32x4 *>(vb + value_at + 16 * d * 64);
+        };
+        if (clean) cs.template values<true>(sc, pf, value, fv, 0);
+        else cs.template values<false>(sc, pf, value, fv, pv_now < 0 ? 0 : t.hi - (c * kChunk + 16 * g));
+    }
+
+    if (!any_col) return;
+    const int64_t slot = at.slot(p);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int cc = wc0 + 16 * n + col;
+        if (!cs.live[n]) continue;
+        const float l = cs.total(n, t.cap);
+        if (t.active <= 1) {
+            const int i = cc / p.group, h = cc - i * p.group;
+            uint16_t *dst = p.out + ((int64_t)(t.r0 + i) * p.heads + at.kvh * p.group + h) * D + 4 * g;
+            const float f = inverse(l, t.first + i);
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) *reinterpret_cast<u32x2 *>(dst + 16 * d) = pack4(cs.o[n][d], f);
+        } else {
+            const int64_t k = slot * p.cols + (cc - t.c0);
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) *reinterpret_cast<f32x4 *>(p.part + k * D + 16 * d + 4 * g) = cs.o[n][d];
+            if (g == 0) {
+                p.ml[k * 2] = cs.max2(n);
+                p.ml[k * 2 + 1] = l;
             }
         }
     }
@@ -444,20 +654,16 @@ __global__ __launch_bounds__(256) void attention_join_kernel(Params p) {
         }
         const int c = t.c0 + cc, i = c / p.group, h = c - i * p.group;
         const float f = inverse(l, t.first + i);
-        u32x2 w;
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            w[j] = (uint32_t)f32_to_f16_bits(a[2 * j] * f) | ((uint32_t)f32_to_f16_bits(a[2 * j + 1] * f) << 16);
-        *reinterpret_cast<u32x2 *>(p.out + ((int64_t)(t.r0 + i) * p.heads + kvh * p.group + h) * D + d) = w;
+        *reinterpret_cast<u32x2 *>(p.out + ((int64_t)(t.r0 + i) * p.heads + kvh * p.group + h) * D + d) = pack4(a, f);
     }
 }
 
 template <int D>
 hipError_t launch(const Params &p, const AttnPlan &plan, hipStream_t stream) {
     const dim3 grid((unsigned)(plan.tiles * p.c.heads * plan.splits));
-    if (plan.shared) attention_kernel<D, 1, true><<<grid, dim3(256), 0, stream>>>(p);
-    else if (plan.nt == 1 || D == 256) attention_kernel<D, 1, false><<<grid, dim3(256), 0, stream>>>(p);
-    else attention_kernel<D, 2, false><<<grid, dim3(256), 0, stream>>>(p);
+    if (plan.shared) attention_token_kernel<D><<<grid, dim3(256), 0, stream>>>(p);
+    else if (plan.nt == 1) attention_rows_kernel<D, 1><<<grid, dim3(256), 0, stream>>>(p);
+    else if constexpr (D <= 128) attention_rows_kernel<D, 2><<<grid, dim3(256), 0, stream>>>(p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || plan.splits <= 1) return e;
     attention_join_kernel<D><<<dim3((unsigned)(plan.tiles * p.c.heads), (unsigned)(plan.cols / 16)), dim3(256), 0, stream>>>(p);
