@@ -32,6 +32,8 @@
 #include "device.h"
 #include "layer.h"
 
+#include <type_traits>
+
 namespace w4a16 {
 namespace {
 
@@ -136,6 +138,8 @@ struct Pages {
         const int id = table[tok >> shift];
         return id < 0 || id >= pages ? -2 : id;
     }
+    // The same where a whole chunk lies in one page.
+    __device__ __forceinline__ int lookup(int c) const { return __builtin_amdgcn_readfirstlane(lookup(c, 0)); }
     __device__ __forceinline__ size_t slot(int page) const { return (size_t)(page < 0 ? 0 : page) * heads + kvh; }
     // byte offset of block x of chunk c within its page's rows of D (keys)
     __device__ __forceinline__ int within(int c, int x) const { return (c * kChunk + 16 * x) & ((1 << shift) - 1); }
@@ -218,10 +222,13 @@ struct Columns {
         }
     }
 
-    // Whether some column does not see all of chunk c.
-    __device__ __forceinline__ bool partial(int c) const {
-        const int lo = c * kChunk;
-        return lo + kChunk - 1 > pos_min || (window && lo <= pos_max - window);
+    // The chunks [lo, hi) of [from, to) that every column sees whole.
+    __device__ __forceinline__ void clean_range(int from, int to, int &lo, int &hi) const {
+        const int end = pos_min < 0 ? 0 : (pos_min + 1) / kChunk;
+        const int start = !window || pos_max < window ? 0 : (pos_max - window) / kChunk + 1;
+        lo = start < from ? from : start > to ? to : start;
+        hi = end > to ? to : end;
+        hi = hi < lo ? lo : hi;
     }
 
     // Masked scores become -inf whatever they hold; a page out of range (of
@@ -332,10 +339,23 @@ struct Columns {
         }
     }
 
-    // Maximum in powers of two, and sum, of this lane's column.
+    // Maximum in powers of two, and sum, of this lane's column; NaN for a row
+    // longer than its table, and where every column saw a page out of range.
     __device__ __forceinline__ float max2(int n) const { return mx[n] * scale; }
-    __device__ __forceinline__ float total(int n, int cap) const {
-        return pos[n] >= cap ? __builtin_nanf("") : l[n][0];  // longer than its table: loud
+    __device__ __forceinline__ float total(int n, int cap, bool lost) const {
+        return lost || pos[n] >= cap ? __builtin_nanf("") : l[n][0];
+    }
+
+    // One chunk.  CLEAN: as for values().  page_v: the page of this lane's 16
+    // tokens.
+    template <bool CLEAN, typename Key, typename Value>
+    __device__ __forceinline__ void chunk(int c, Key key, float fk, Value value, float fv, int page_v) {
+        f32x4 sc[NT][4];
+        f16x8 pf[NT][2];
+        scores(sc, key, fk);
+        if constexpr (!CLEAN) mask(sc, c, page_v == -2);
+        weights(sc, pf);
+        values<CLEAN>(sc, pf, value, fv, page_v < 0 ? 0 : hi - (c * kChunk + 16 * (int)((threadIdx.x & 63) >> 4)));
     }
 };
 
@@ -416,12 +436,15 @@ __global__ __launch_bounds__(256, (D == 64 ? 3 : D == 128 ? 2 : 1)) void attenti
             pv_next = pages.lookup(c + 4, g);
         }
     }
-    for (; c < chi; c += 4) {
-        const bool more = c + 4 < chi, bad = __any(pk == -2 || pv == -2);
+    bool lost = false;
+    auto turn = [&](auto clean) __attribute__((always_inline)) {
+        const bool more = c + 4 < chi;
+        int pk_after = -1, pv_after = -1;
+        const int page_v = pv;
+        if constexpr (decltype(clean)::value) lost = lost || __any(pk == -2 || pv == -2);
         f32x4 sc[1][4];
         f16x8 pf[1][2];
         cs.scores(sc, [&](int x, int m) { return kr[x][m]; }, scale_of((uint8_t)bk));
-        int pk_after = -1, pv_after = -1;
         if (more) {
             load_keys(c + 4, pk_next);
             if (c + 8 < chi) {
@@ -429,18 +452,21 @@ __global__ __launch_bounds__(256, (D == 64 ? 3 : D == 128 ? 2 : 1)) void attenti
                 pv_after = pages.lookup(c + 8, g);
             }
         }
-        const bool clean = !cs.partial(c) && !bad;
-        if (!clean) cs.mask(sc, c, pv == -2);
+        if constexpr (!decltype(clean)::value) cs.mask(sc, c, page_v == -2);
         cs.weights(sc, pf);
-        auto value = [&](int d) { return vr[d]; };
-        if (clean) cs.template values<true>(sc, pf, value, scale_of((uint8_t)bv), 0);
-        else cs.template values<false>(sc, pf, value, scale_of((uint8_t)bv), pv < 0 ? 0 : t.hi - (c * kChunk + 16 * g));
+        cs.template values<decltype(clean)::value>(sc, pf, [&](int d) { return vr[d]; }, scale_of((uint8_t)bv),
+                                                   page_v < 0 ? 0 : t.hi - (c * kChunk + 16 * g));
         if (more) load_values(c + 4, pv_next);
         pk = pk_next;
         pv = pv_next;
         pk_next = pk_after;
         pv_next = pv_after;
-    }
+    };
+    int clean_lo, clean_hi;
+    cs.clean_range(clo, chi, clean_lo, clean_hi);
+    for (; c < clean_lo; c += 4) turn(std::false_type{});
+    for (; c < clean_hi; c += 4) turn(std::true_type{});
+    for (; c < chi; c += 4) turn(std::false_type{});
 
     // The waves' pieces meet in LDS, in wave order.
 #pragma unroll
@@ -448,7 +474,7 @@ __global__ __launch_bounds__(256, (D == 64 ? 3 : D == 128 ? 2 : 1)) void attenti
         *reinterpret_cast<f32x4 *>(&lds_o[(wave * 16 + col) * D + 16 * d + 4 * g]) = cs.o[0][d];
     if (g == 0) {
         lds_ml[(wave * 16 + col) * 2] = cs.max2(0);
-        lds_ml[(wave * 16 + col) * 2 + 1] = cs.total(0, t.cap);
+        lds_ml[(wave * 16 + col) * 2 + 1] = cs.total(0, t.cap, lost);
     }
     __syncthreads();
     const int64_t slot = at.slot(p);
@@ -500,7 +526,8 @@ __device__ __forceinline__ void load_to_lds16(const uint8_t *src, uint32_t to) {
 // eight lanes of a read phase, which want the same piece of different rows,
 // meet different banks.  Direct loads write in lane order, so the exchange is
 // made in the lanes' addresses.
-template <int D, int NT>
+// ONE: a chunk lies in one page (pages of 64 tokens or more).
+template <int D, int NT, bool ONE>
 __global__ __launch_bounds__(256, (D <= 128 ? 2 : 1)) void attention_rows_kernel(Params p) {
     constexpr int PR = D / 16;             // pieces per token of keys
     constexpr int LOADS = D / 64;          // direct loads per wave of keys, and of values
@@ -552,58 +579,70 @@ __global__ __launch_bounds__(256, (D <= 128 ? 2 : 1)) void attention_rows_kernel
     for (int m = 0; m < D / 64; ++m) key_at[m] = (16 * kx + (col & 3)) * D + 16 * ((4 * m + g) ^ key_turn(16 * kx + (col & 3)));
     const int value_at = col * 64 + 16 * (g ^ ((col >> 1) & 3));
 
-    // Pages and scale bytes run ahead of the chunks they belong to.
-    int pw = -1, pl = -1, pk = -1, pv = -1, pk_next = -1, pv_next = -1;
-    uint32_t bk = 0, bv = 0;
-    if (clo < chi) {
-        stage(clo, pages.lookup(clo, wave), pages.lookup(clo, vx));
-        pk = pages.lookup(clo, kx);
-        pv = pages.lookup(clo, g);
-        bk = p.c.k_scale[pages.slot(pk)];
-        bv = p.c.v_scale[pages.slot(pv)];
-        if (clo + 1 < chi) {
-            pw = pages.lookup(clo + 1, wave);
-            pl = pages.lookup(clo + 1, vx);
-            pk_next = pages.lookup(clo + 1, kx);
-            pv_next = pages.lookup(clo + 1, g);
+    // Pages and scale bytes run ahead of the chunks they belong to: those that
+    // this wave loads keys and values of, and those of the keys and values that
+    // this lane multiplies.
+    struct Ids {
+        int load_k, load_v, k, v;
+    };
+    auto ids = [&](int c) __attribute__((always_inline)) {
+        if constexpr (ONE) {
+            const int id = pages.lookup(c);
+            // of a chunk that ends inside the tile's tokens, blocks past them
+            // count as the page's: their scores are masked
+            return Ids{id, id, id, id};
+        } else {
+            return Ids{pages.lookup(c, wave), pages.lookup(c, vx), pages.lookup(c, kx), pages.lookup(c, g)};
         }
+    };
+    Ids now{-1, -1, -1, -1}, next = now;
+    uint32_t bk = 0, bv = 0;
+    auto scale_bytes = [&]() __attribute__((always_inline)) {
+        bk = p.c.k_scale[pages.slot(next.k)];
+        bv = p.c.v_scale[pages.slot(next.v)];
+    };
+    if (clo < chi) {
+        next = ids(clo);
+        stage(clo, next.load_k, next.load_v);
+        scale_bytes();
+        now = next;
+        if (clo + 1 < chi) next = ids(clo + 1);
     }
-    for (int c = clo; c < chi; ++c) {
+    bool lost = false;
+    auto turn = [&](int c, auto clean) __attribute__((always_inline)) {
         // chunk c has landed, and every wave is done with the other buffer
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         const float fk = scale_of((uint8_t)bk), fv = scale_of((uint8_t)bv);
-        const int pk_now = pk, pv_now = pv;
+        const Ids cur = now;
         if (c + 1 < chi) {
-            stage(c + 1, pw, pl);
-            pk = pk_next;
-            pv = pv_next;
-            bk = p.c.k_scale[pages.slot(pk)];
-            bv = p.c.v_scale[pages.slot(pv)];
-            if (c + 2 < chi) {
-                pw = pages.lookup(c + 2, wave);
-                pl = pages.lookup(c + 2, vx);
-                pk_next = pages.lookup(c + 2, kx);
-                pv_next = pages.lookup(c + 2, g);
-            }
+            stage(c + 1, next.load_k, next.load_v);
+            scale_bytes();
+            now = next;
+            if (c + 2 < chi) next = ids(c + 2);
         }
-        if (c < own_lo || c >= own_hi) continue;
         const uint8_t *kb = &lds[c & 1][0], *vb = kb + HALF;
-        f32x4 sc[NT][4];
-        f16x8 pf[NT][2];
-        cs.scores(sc, [&](int x, int m) __attribute__((always_inline)) {
+        auto key = [&](int x, int m) __attribute__((always_inline)) {
             return *reinterpret_cast<const u32x4 *>(kb + key_at[m] + 4 * x * D);
-        }, fk);
-        const bool clean = !cs.partial(c) && !__any(pk_now == -2 || pv_now == -2);
-        if (!clean) cs.mask(sc, c, pv_now == -2);
-        cs.weights(sc, pf);
+        };
         auto value = [&](int d) __attribute__((always_inline)) {
             return *reinterpret_cast<const u32x4 *>(vb + value_at + 16 * d * 64);
         };
-        if (clean) cs.template values<true>(sc, pf, value, fv, 0);
-        else cs.template values<false>(sc, pf, value, fv, pv_now < 0 ? 0 : t.hi - (c * kChunk + 16 * g));
-    }
+        if constexpr (decltype(clean)::value) {
+            lost = lost || (ONE ? cur.k == -2 : (bool)__any(cur.k == -2 || cur.v == -2));
+            cs.template chunk<true>(c, key, fk, value, fv, cur.v);
+        } else if (c >= own_lo && c < own_hi) {
+            cs.template chunk<false>(c, key, fk, value, fv, cur.v);
+        }
+    };
+    int clean_lo, clean_hi;
+    cs.clean_range(clo, chi, clean_lo, clean_hi);
+    if (!any_col) clean_lo = clean_hi = chi;
+    int c = clo;
+    for (; c < clean_lo; ++c) turn(c, std::false_type{});
+    for (; c < clean_hi; ++c) turn(c, std::true_type{});
+    for (; c < chi; ++c) turn(c, std::false_type{});
 
     if (!any_col) return;
     const int64_t slot = at.slot(p);
@@ -611,7 +650,7 @@ __global__ __launch_bounds__(256, (D <= 128 ? 2 : 1)) void attention_rows_kernel
     for (int n = 0; n < NT; ++n) {
         const int cc = wc0 + 16 * n + col;
         if (!cs.live[n]) continue;
-        const float l = cs.total(n, t.cap);
+        const float l = cs.total(n, t.cap, lost);
         if (t.active <= 1) {
             const int i = cc / p.group, h = cc - i * p.group;
             uint16_t *dst = p.out + ((int64_t)(t.r0 + i) * p.heads + at.kvh * p.group + h) * D + 4 * g;
@@ -662,8 +701,12 @@ template <int D>
 hipError_t launch(const Params &p, const AttnPlan &plan, hipStream_t stream) {
     const dim3 grid((unsigned)(plan.tiles * p.c.heads * plan.splits));
     if (plan.shared) attention_token_kernel<D><<<grid, dim3(256), 0, stream>>>(p);
-    else if (plan.nt == 1) attention_rows_kernel<D, 1><<<grid, dim3(256), 0, stream>>>(p);
-    else if constexpr (D <= 128) attention_rows_kernel<D, 2><<<grid, dim3(256), 0, stream>>>(p);
+    else if (plan.nt == 1 && p.c.page_shift >= 6) attention_rows_kernel<D, 1, true><<<grid, dim3(256), 0, stream>>>(p);
+    else if (plan.nt == 1) attention_rows_kernel<D, 1, false><<<grid, dim3(256), 0, stream>>>(p);
+    else if constexpr (D <= 128) {
+        if (p.c.page_shift >= 6) attention_rows_kernel<D, 2, true><<<grid, dim3(256), 0, stream>>>(p);
+        else attention_rows_kernel<D, 2, false><<<grid, dim3(256), 0, stream>>>(p);
+    }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || plan.splits <= 1) return e;
     attention_join_kernel<D><<<dim3((unsigned)(plan.tiles * p.c.heads), (unsigned)(plan.cols / 16)), dim3(256), 0, stream>>>(p);
