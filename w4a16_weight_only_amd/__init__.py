@@ -134,9 +134,15 @@ def _check(rc: int) -> None:
         raise W4A16Error(rc, lib().w4a16_last_error().decode())
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream_ptr(dev):
@@ -148,6 +154,8 @@ def _dev_tensor(t, name, dtype, ndim):
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype is dtype and t.dim() == ndim and t.is_cuda and t.is_contiguous():
+        return t
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if t.dim() != ndim:
@@ -356,7 +364,7 @@ def w4a16_release():
 # ------------------------------------------- decoder-layer operators, 8 bits ---
 
 def _row_tensor(t, name):
-    """fp16 rows with unit stride along the last dimension; the row stride is free."""
+    """Row stride of fp16 rows with unit stride along the last dimension."""
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
@@ -366,25 +374,33 @@ def _row_tensor(t, name):
         raise ValueError("%s must be 2-D, got shape %s" % (name, tuple(t.shape)))
     if not t.is_cuda:
         raise ValueError("%s must be on the GPU" % name)
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    ld, unit = t.stride()
+    rows, width = t.shape
+    if unit != 1 and width > 1:
         raise ValueError("%s must have unit stride along its last dimension" % name)
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return ld if rows > 1 else width
 
 
-def _same_device(first, **others):
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError("%s is on %s, not on %s" % (name, t.device, first.device))
+def _same_device(first, *others):
+    dev = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("a tensor is on %s, not on %s like the first" % (t.device, first.device))
 
 
-def _launch(dev, fn, *args):
-    """fn(*args, stream) on the tensors' device and torch's current stream there."""
+def _launch(first, fn, *args):
+    """fn(*args, stream) on the first tensor's device and torch's current stream there."""
     torch = _torch()
-    if dev.index is not None and dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            _check(fn(*args, _stream_ptr(dev)))
+    dev = first.get_device()
+    # the current stream's handle without a Stream object around it
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if dev == torch._C._cuda_getDevice():
+        rc = fn(*args, stream)
     else:
-        _check(fn(*args, _stream_ptr(dev)))
+        with torch.cuda.device(dev):
+            rc = fn(*args, stream)
+    if rc != 0:
+        _check(rc)
 
 
 def _ptr(t):
@@ -415,7 +431,7 @@ def _norm_args(x, residual, weight, sum_out):
         _dev_tensor(sum_out, "sum_out", torch.float16, 2)
         if tuple(sum_out.shape) != (M, W):
             raise ValueError("sum_out must be [M, width] = [%d, %d]" % (M, W))
-    _same_device(x, residual=residual, weight=weight, sum_out=sum_out)
+    _same_device(x, residual, weight, sum_out)
     return ldx, ldr, M, W, sum_out
 
 
@@ -431,8 +447,8 @@ def w4a16_add_rmsnorm(x, residual=None, weight=None, eps=1e-6, out=None, sum_out
         _dev_tensor(out, "out", torch.float16, 2)
         if tuple(out.shape) != (M, W):
             raise ValueError("out must be [M, width] = [%d, %d]" % (M, W))
-        _same_device(x, out=out)
-    _launch(x.device, lib().w4a16_add_rmsnorm, x.data_ptr(), ldx, _ptr(residual), ldr, _ptr(weight), eps, M, W,
+        _same_device(x, out)
+    _launch(x, lib().w4a16_add_rmsnorm, x.data_ptr(), ldx, _ptr(residual), ldr, _ptr(weight), eps, M, W,
             _ptr(sum_out), out.data_ptr(), None, None)
     return out, x if sum_out is None else sum_out
 
@@ -456,8 +472,8 @@ def w4a16_add_rmsnorm_fp8(x, residual=None, weight=None, eps=1e-6, out=None, sum
     scale fp32 [M, ceil(width/128)] per row and block of 128 columns."""
     ldx, ldr, M, W, sum_out = _norm_args(x, residual, weight, sum_out)
     codes, scales = _codes_out(out, M, W, x.device)
-    _same_device(x, codes=codes, scales=scales)
-    _launch(x.device, lib().w4a16_add_rmsnorm, x.data_ptr(), ldx, _ptr(residual), ldr, _ptr(weight), eps, M, W,
+    _same_device(x, codes, scales)
+    _launch(x, lib().w4a16_add_rmsnorm, x.data_ptr(), ldx, _ptr(residual), ldr, _ptr(weight), eps, M, W,
             _ptr(sum_out), None, codes.data_ptr(), scales.data_ptr())
     return (codes, scales), x if sum_out is None else sum_out
 
@@ -473,8 +489,8 @@ def w4a16_quant_fp8(x, act=ACT_NONE, out=None):
             raise ValueError("SwiGLU takes rows of gate and up halves, got width %d" % K)
         K //= 2
     codes, scales = _codes_out(out, M, K, x.device)
-    _same_device(x, codes=codes, scales=scales)
-    _launch(x.device, lib().w4a16_quant_fp8, act, x.data_ptr(), ldx, M, K, codes.data_ptr(), scales.data_ptr())
+    _same_device(x, codes, scales)
+    _launch(x, lib().w4a16_quant_fp8, act, x.data_ptr(), ldx, M, K, codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
@@ -501,8 +517,8 @@ def w4a16_gemm_fp8(a, a_scales, b, b_scales, out=None):
         _dev_tensor(out, "out", torch.float16, 2)
         if tuple(out.shape) != (M, N):
             raise ValueError("out must be [M, N] = [%d, %d]" % (M, N))
-    _same_device(a, a_scales=a_scales, b=b, b_scales=b_scales, out=out)
-    _launch(a.device, lib().w4a16_gemm_fp8, a.data_ptr(), a_scales.data_ptr(), b.data_ptr(), b_scales.data_ptr(), M, K,
+    _same_device(a, a_scales, b, b_scales, out)
+    _launch(a, lib().w4a16_gemm_fp8, a.data_ptr(), a_scales.data_ptr(), b.data_ptr(), b_scales.data_ptr(), M, K,
             N, out.data_ptr())
     return out
 
@@ -537,7 +553,7 @@ def _cache_struct(cache):
     if tuple(v.shape) != (P, H, D, page) or tuple(ks.shape) != (P, H) or tuple(vs.shape) != (P, H):
         raise ValueError("cache must hold k [pages, heads, page, dim], v [pages, heads, dim, page] and scales "
                          "[pages, heads]")
-    _same_device(k, v=v, k_scale=ks, v_scale=vs)
+    _same_device(k, v, ks, vs)
     return KVCache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), P, H, page, D)
 
 
@@ -569,8 +585,8 @@ def w4a16_kv_append(k, v, cache, block_table, lens, rows=None):
         raise ValueError("k and v must be [T, heads*dim] = [*, %d], got %s and %s"
                          % (c.heads * c.dim, tuple(k.shape), tuple(v.shape)))
     B, width = _sequence_args(block_table, lens, rows, T)
-    _same_device(k, v=v, cache=cache["k"], block_table=block_table, lens=lens, rows=rows)
-    _launch(k.device, lib().w4a16_kv_append, k.data_ptr(), ldk, v.data_ptr(), ldv, ctypes.byref(c),
+    _same_device(k, v, cache["k"], block_table, lens, rows)
+    _launch(k, lib().w4a16_kv_append, k.data_ptr(), ldk, v.data_ptr(), ldv, ctypes.byref(c),
             block_table.data_ptr(), width, lens.data_ptr(), _ptr(rows), B, T)
     return cache
 
@@ -605,8 +621,8 @@ def w4a16_attention(q, cache, block_table, lens, rows=None, scale=None, window=0
         need = lib().w4a16_attention_workspace_bytes(heads, ref, width, B, T)
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    _same_device(q, cache=cache["k"], block_table=block_table, lens=lens, rows=rows, out=out, workspace=workspace)
-    _launch(q.device, lib().w4a16_attention, q.data_ptr(), ldq, heads, ref, block_table.data_ptr(), width,
+    _same_device(q, cache["k"], block_table, lens, rows, out, workspace)
+    _launch(q, lib().w4a16_attention, q.data_ptr(), ldq, heads, ref, block_table.data_ptr(), width,
             lens.data_ptr(), _ptr(rows), B, T, c.dim ** -0.5 if scale is None else scale, window, out.data_ptr(),
             _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size())
     return out
@@ -647,10 +663,8 @@ def w4a16_decode_step_kv(stack, caches, block_table, lens, x, scale=None, out=No
         _dev_tensor(out, "out", torch.float16, 2)
         if out.shape != x.shape:
             raise ValueError("out must be [M, H] = [%d, %d]" % tuple(x.shape))
-    _same_device(x, block_table=block_table, lens=lens, out=out, workspace=workspace,
-                 **{"stack[%d]" % i: L["b_packed"] for i, L in enumerate(stack)},
-                 **{"caches[%d]" % i: c["k"] for i, c in enumerate(caches)})
-    _launch(x.device, lib().w4a16_decode_step_kv, lp, len(caches), cp, block_table.data_ptr(), width, lens.data_ptr(),
+    _same_device(x, block_table, lens, out, workspace, *[L["b_packed"] for L in stack], *[c["k"] for c in caches])
+    _launch(x, lib().w4a16_decode_step_kv, lp, len(caches), cp, block_table.data_ptr(), width, lens.data_ptr(),
             carr[0].dim ** -0.5 if scale is None else scale, x.data_ptr(), out.data_ptr(), M, workspace.data_ptr(),
             workspace.numel() * workspace.element_size())
     return out

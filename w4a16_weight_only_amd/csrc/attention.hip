@@ -87,18 +87,23 @@ struct Tile {
 __device__ __forceinline__ Tile make_tile(const Params &p, int tile) {
     Tile t;
     const int cols = p.cols;
-    auto start = [&](int b) {
-        int r = b;
-        if (p.s.rows) {
-            r = p.s.rows[b];
+    int64_t first_tile;
+    if (!p.s.rows) {
+        const int per = (p.group + cols - 1) / cols;
+        t.b = tile / per;
+        first_tile = (int64_t)t.b * per;
+    } else {
+        auto start = [&](int b) {
+            int r = p.s.rows[b];
             r = r < 0 ? 0 : r > p.s.T ? p.s.T : r;
-        }
-        return (int64_t)((uint32_t)(r * p.group) / (uint32_t)cols) + b;
-    };
-    t.b = find_sequence(p.s.B, tile, start);
+            return (int64_t)((uint32_t)(r * p.group) / (uint32_t)cols) + b;
+        };
+        t.b = find_sequence(p.s.B, tile, start);
+        first_tile = start(t.b);
+    }
     sequence_rows(p.s, t.b, t.r0, t.n);
     t.ncols = t.n * p.group;
-    const int64_t c0 = (tile - start(t.b)) * cols;  // negative only for a malformed offset table
+    const int64_t c0 = (tile - first_tile) * cols;  // negative only for a malformed offset table
     t.c0 = c0 < 0 || c0 >= t.ncols ? t.ncols : (int)c0;
     const int64_t len = p.s.lens[t.b] < 0 ? 0 : p.s.lens[t.b];
     t.first = (int)(len - t.n);
@@ -109,7 +114,7 @@ __device__ __forceinline__ Tile make_tile(const Params &p, int tile) {
     const int64_t lo = p.window ? (int64_t)t.first + t.c0 / p.group - p.window + 1 : 0;
     t.hi = (int)(hi < 0 ? 0 : hi > t.cap ? t.cap : hi);
     t.lo = (int)(lo < 0 ? 0 : lo > t.hi ? t.hi : lo);
-    t.split0 = t.lo / kChunk;
+    t.split0 = p.window ? t.lo / kChunk : 0;
     const int chunks = t.hi > t.lo ? (t.hi + kChunk - 1) / kChunk - t.split0 : 0;
     t.active = (chunks + p.quota - 1) / p.quota;
     return t;
@@ -128,15 +133,16 @@ __device__ __forceinline__ float inverse(float l, int pos) {
 struct Pages {
     const int32_t *table;
     int64_t pages;
-    int heads, kvh, shift, hi;
+    int heads, kvh, shift, hi, last;
     __device__ __forceinline__ Pages(const Params &p, const Tile &t, int kvh_)
         : table(p.s.table + (int64_t)t.b * p.s.max_pages), pages(p.c.pages), heads(p.c.heads), kvh(kvh_),
-          shift(p.c.page_shift), hi(t.hi) {}
+          shift(p.c.page_shift), hi(t.hi), last(p.s.max_pages - 1) {}
+    // (The table is read at any place inside it, so that the read need not
+    // wait for the sequence's length.)
     __device__ __forceinline__ int lookup(int c, int x) const {
-        const int tok = c * kChunk + 16 * x;
-        if (tok >= hi) return -1;
-        const int id = table[tok >> shift];
-        return id < 0 || id >= pages ? -2 : id;
+        const int tok = c * kChunk + 16 * x, at = tok >> shift;
+        const int id = table[at < last ? at : last];
+        return tok >= hi ? -1 : id < 0 || id >= pages ? -2 : id;
     }
     // The same where a whole chunk lies in one page.
     __device__ __forceinline__ int lookup(int c) const { return __builtin_amdgcn_readfirstlane(lookup(c, 0)); }
@@ -250,17 +256,23 @@ struct Columns {
     // Weights of a chunk, rounded to fp16.  The running maxima are raised when
     // a score passes them by kLazy after its scale.
     __device__ __forceinline__ void weights(const f32x4 (&sc)[NT][4], f16x8 (&pf)[NT][2]) {
+        float top[NT];
+        bool raise = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            float top = -__builtin_inff();
+            top[n] = -__builtin_inff();
 #pragma unroll
             for (int x = 0; x < 4; ++x)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[n][x][i]);
-            if (__any(top > mx[n] + lazy)) {
-                top = fmaxf(top, __shfl_xor(top, 16));
-                top = fmaxf(top, __shfl_xor(top, 32));
-                const float m = fmaxf(mx[n], top);
+                for (int i = 0; i < 4; ++i) top[n] = fmaxf(top[n], sc[n][x][i]);
+            raise = raise || top[n] > mx[n] + lazy;
+        }
+        if (__any(raise)) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                top[n] = fmaxf(top[n], __shfl_xor(top[n], 16));
+                top[n] = fmaxf(top[n], __shfl_xor(top[n], 32));
+                const float m = fmaxf(mx[n], top[n]);
                 const float f = m == mx[n] ? 1.0f : __builtin_amdgcn_exp2f((mx[n] - m) * scale);
                 mx[n] = m;
 #pragma unroll
@@ -270,6 +282,9 @@ struct Columns {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o[n][d][i] *= f;
             }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
             const float base = mx[n] == -__builtin_inff() ? 0.f : mx[n] * scale;
 #pragma unroll
             for (int x = 0; x < 4; ++x)
@@ -352,10 +367,16 @@ struct Columns {
     __device__ __forceinline__ void chunk(int c, Key key, float fk, Value value, float fv, int page_v) {
         f32x4 sc[NT][4];
         f16x8 pf[NT][2];
+        // matrix instructions first: the other wave of the SIMD does its softmax
+        // meanwhile (prompts 627 -> 619 us)
+        __builtin_amdgcn_s_setprio(1);
         scores(sc, key, fk);
+        __builtin_amdgcn_s_setprio(0);
         if constexpr (!CLEAN) mask(sc, c, page_v == -2);
         weights(sc, pf);
+        __builtin_amdgcn_s_setprio(1);
         values<CLEAN>(sc, pf, value, fv, page_v < 0 ? 0 : hi - (c * kChunk + 16 * (int)((threadIdx.x & 63) >> 4)));
+        __builtin_amdgcn_s_setprio(0);
     }
 };
 
@@ -383,7 +404,7 @@ struct Place {
     }
 };
 
-// Few columns (single tokens): the workgroup's four waves hold the same 16
+// Few columns (single tokens): the workgroup's waves hold the same 16
 // columns and take chunks in turn, keys and values straight from memory into
 // registers.  Bound by reading the cache.  The loop is pipelined: a chunk's
 // keys are requested when those of the chunk before have been multiplied, its
@@ -391,9 +412,10 @@ struct Place {
 // chunk earlier still.
 template <int D>
 __global__ __launch_bounds__(256, (D == 64 ? 3 : D == 128 ? 2 : 1)) void attention_token_kernel(Params p) {
+    constexpr int W = 4;
     constexpr int KD = D / 64, DT = D / 16;
-    __shared__ __align__(16) float lds_o[4 * 16 * D];
-    __shared__ float lds_ml[4 * 16 * 2];
+    __shared__ __align__(16) float lds_o[W * 16 * D];
+    __shared__ float lds_ml[W * 16 * 2];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, g = lane >> 4, kx = col >> 2;
     const Place at(p);
     const Tile t = make_tile(p, at.tile);
@@ -431,14 +453,14 @@ __global__ __launch_bounds__(256, (D == 64 ? 3 : D == 128 ? 2 : 1)) void attenti
         pv = pages.lookup(c, g);
         load_keys(c, pk);
         load_values(c, pv);
-        if (c + 4 < chi) {
-            pk_next = pages.lookup(c + 4, kx);
-            pv_next = pages.lookup(c + 4, g);
+        if (c + W < chi) {
+            pk_next = pages.lookup(c + W, kx);
+            pv_next = pages.lookup(c + W, g);
         }
     }
     bool lost = false;
     auto turn = [&](auto clean) __attribute__((always_inline)) {
-        const bool more = c + 4 < chi;
+        const bool more = c + W < chi;
         int pk_after = -1, pv_after = -1;
         const int page_v = pv;
         if constexpr (decltype(clean)::value) lost = lost || __any(pk == -2 || pv == -2);
@@ -446,17 +468,17 @@ __global__ __launch_bounds__(256, (D == 64 ? 3 : D == 128 ? 2 : 1)) void attenti
         f16x8 pf[1][2];
         cs.scores(sc, [&](int x, int m) { return kr[x][m]; }, scale_of((uint8_t)bk));
         if (more) {
-            load_keys(c + 4, pk_next);
-            if (c + 8 < chi) {
-                pk_after = pages.lookup(c + 8, kx);
-                pv_after = pages.lookup(c + 8, g);
+            load_keys(c + W, pk_next);
+            if (c + 2 * W < chi) {
+                pk_after = pages.lookup(c + 2 * W, kx);
+                pv_after = pages.lookup(c + 2 * W, g);
             }
         }
         if constexpr (!decltype(clean)::value) cs.mask(sc, c, page_v == -2);
         cs.weights(sc, pf);
         cs.template values<decltype(clean)::value>(sc, pf, [&](int d) { return vr[d]; }, scale_of((uint8_t)bv),
                                                    page_v < 0 ? 0 : t.hi - (c * kChunk + 16 * g));
-        if (more) load_values(c + 4, pv_next);
+        if (more) load_values(c + W, pv_next);
         pk = pk_next;
         pv = pv_next;
         pk_next = pk_after;
@@ -464,9 +486,9 @@ __global__ __launch_bounds__(256, (D == 64 ? 3 : D == 128 ? 2 : 1)) void attenti
     };
     int clean_lo, clean_hi;
     cs.clean_range(clo, chi, clean_lo, clean_hi);
-    for (; c < clean_lo; c += 4) turn(std::false_type{});
-    for (; c < clean_hi; c += 4) turn(std::true_type{});
-    for (; c < chi; c += 4) turn(std::false_type{});
+    for (; c < clean_lo; c += W) turn(std::false_type{});
+    for (; c < clean_hi; c += W) turn(std::true_type{});
+    for (; c < chi; c += W) turn(std::false_type{});
 
     // The waves' pieces meet in LDS, in wave order.
 #pragma unroll
@@ -478,16 +500,16 @@ __global__ __launch_bounds__(256, (D == 64 ? 3 : D == 128 ? 2 : 1)) void attenti
     }
     __syncthreads();
     const int64_t slot = at.slot(p);
-    for (int x = threadIdx.x; x < 16 * D / 4; x += 256) {
+    for (int x = threadIdx.x; x < 16 * D / 4; x += 64 * W) {
         const int cc = x / (D / 4), d = (x - cc * (D / 4)) * 4;
         if (t.c0 + cc >= t.ncols) continue;
         float m = -__builtin_inff();
 #pragma unroll
-        for (int w = 0; w < 4; ++w) m = fmaxf(m, lds_ml[(w * 16 + cc) * 2]);
+        for (int w = 0; w < W; ++w) m = fmaxf(m, lds_ml[(w * 16 + cc) * 2]);
         f32x4 a{0.f, 0.f, 0.f, 0.f};
         float l = 0.f;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
+        for (int w = 0; w < W; ++w) {
             const float mw = lds_ml[(w * 16 + cc) * 2], lw = lds_ml[(w * 16 + cc) * 2 + 1];
             const float f = mw == -__builtin_inff() ? (lw == 0.f ? 0.f : 1.f) : __builtin_amdgcn_exp2f(mw - m);
             const f32x4 v = *reinterpret_cast<const f32x4 *>(&lds_o[(w * 16 + cc) * D + d]);
@@ -669,32 +691,51 @@ __global__ __launch_bounds__(256, (D <= 128 ? 2 : 1)) void attention_rows_kernel
     }
 }
 
-// Joins a column tile's pieces: 16 columns per workgroup, 4 dims per thread.
+// Joins a column's pieces: one workgroup per column, D / 4 threads to a piece,
+// the 1024 / D groups of threads taking pieces in turn and meeting in LDS, in
+// order.
 template <int D>
 __global__ __launch_bounds__(256) void attention_join_kernel(Params p) {
-    const int kvh = blockIdx.x % p.c.heads, tile = blockIdx.x / p.c.heads;
+    constexpr int TP = D / 4, GROUPS = 256 / TP;
+    __shared__ f32x4 sh_o[GROUPS][TP];
+    __shared__ float sh_l[GROUPS], sh_m[4];
+    const int kvh = blockIdx.x % p.c.heads, tile = blockIdx.x / p.c.heads, cc = blockIdx.y;
     const Tile t = make_tile(p, tile);
-    if (t.active <= 1) return;
+    if (t.active <= 1 || t.c0 + cc >= t.ncols) return;
     const int64_t slot = ((int64_t)tile * p.c.heads + kvh) * p.splits;
-    for (int x = threadIdx.x; x < 16 * D / 4; x += 256) {
-        const int cc = blockIdx.y * 16 + x / (D / 4), d = (x % (D / 4)) * 4;
-        if (t.c0 + cc >= t.ncols) continue;
-        float m = -__builtin_inff();
-        for (int s = 0; s < t.active; ++s) m = fmaxf(m, p.ml[((slot + s) * p.cols + cc) * 2]);
-        f32x4 a{0.f, 0.f, 0.f, 0.f};
-        float l = 0.f;
-        for (int s = 0; s < t.active; ++s) {
-            const float ms = p.ml[((slot + s) * p.cols + cc) * 2], ls = p.ml[((slot + s) * p.cols + cc) * 2 + 1];
-            const float f = ms == -__builtin_inff() ? (ls == 0.f ? 0.f : 1.f) : __builtin_amdgcn_exp2f(ms - m);
-            const f32x4 v = *reinterpret_cast<const f32x4 *>(p.part + ((slot + s) * p.cols + cc) * D + d);
-            l += ls * f;
+    const float *ml = p.ml + (slot * p.cols + cc) * 2, *part = p.part + (slot * p.cols + cc) * D;
+    float m = -__builtin_inff();
+    for (int s = threadIdx.x; s < t.active; s += 256) m = fmaxf(m, ml[(int64_t)s * p.cols * 2]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) a[j] = __builtin_fmaf(v[j], f, a[j]);
-        }
-        const int c = t.c0 + cc, i = c / p.group, h = c - i * p.group;
-        const float f = inverse(l, t.first + i);
-        *reinterpret_cast<u32x2 *>(p.out + ((int64_t)(t.r0 + i) * p.heads + kvh * p.group + h) * D + d) = pack4(a, f);
+    for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+    if ((threadIdx.x & 63) == 0) sh_m[threadIdx.x >> 6] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(sh_m[0], sh_m[1]), fmaxf(sh_m[2], sh_m[3]));
+    const int group = threadIdx.x / TP, d = threadIdx.x % TP;
+    f32x4 a{0.f, 0.f, 0.f, 0.f};
+    float l = 0.f;
+#pragma unroll 4
+    for (int s = group; s < t.active; s += GROUPS) {
+        const float ms = ml[(int64_t)s * p.cols * 2], ls = ml[(int64_t)s * p.cols * 2 + 1];
+        const f32x4 v = *reinterpret_cast<const f32x4 *>(part + (int64_t)s * p.cols * D + 4 * d);
+        const float f = ms == -__builtin_inff() ? (ls == 0.f ? 0.f : 1.f) : __builtin_amdgcn_exp2f(ms - m);
+        l = __builtin_fmaf(ls, f, l);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a[j] = __builtin_fmaf(v[j], f, a[j]);
     }
+    sh_o[group][d] = a;
+    if (d == 0) sh_l[group] = l;
+    __syncthreads();
+    if (group != 0) return;
+#pragma unroll
+    for (int k = 1; k < GROUPS; ++k) {
+        l += sh_l[k];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a[j] += sh_o[k][d][j];
+    }
+    const int c = t.c0 + cc, i = c / p.group, h = c - i * p.group;
+    *reinterpret_cast<u32x2 *>(p.out + ((int64_t)(t.r0 + i) * p.heads + kvh * p.group + h) * D + 4 * d) =
+        pack4(a, inverse(l, t.first + i));
 }
 
 template <int D>
@@ -709,26 +750,38 @@ hipError_t launch(const Params &p, const AttnPlan &plan, hipStream_t stream) {
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || plan.splits <= 1) return e;
-    attention_join_kernel<D><<<dim3((unsigned)(plan.tiles * p.c.heads), (unsigned)(plan.cols / 16)), dim3(256), 0, stream>>>(p);
+    attention_join_kernel<D><<<dim3((unsigned)(plan.tiles * p.c.heads), (unsigned)plan.join_cols), dim3(256), 0, stream>>>(p);
     return hipGetLastError();
 }
 
 }  // namespace
 
 AttnPlan plan_attention(int64_t heads, int64_t kv_heads, int64_t dim, int64_t page, int64_t max_pages, int64_t B,
-                        int64_t T) {
+                        int64_t T, bool single) {
     AttnPlan p;
     const int64_t group = heads / kv_heads;
     const int64_t per = (T * group + B - 1) / B;  // columns of the average sequence
     p.shared = per <= 16;
     p.nt = p.shared || per <= 64 || dim == 256 ? 1 : 2;
     p.cols = p.shared ? 16 : 64 * p.nt;
-    p.tiles = T * group / p.cols + B;
+    // ragged rows: an upper bound, sequence b's tiles beginning at
+    // floor(rows[b] * group / cols) + b
+    p.tiles = single ? B * ((group + p.cols - 1) / p.cols) : T * group / p.cols + B;
+    p.join_cols = (int)(single && group < p.cols ? group : p.cols);
     const int64_t chunks = (max_pages * page + kChunk - 1) / kChunk;
     const int64_t wgs = p.tiles * kv_heads;
-    int64_t splits = (1024 + wgs - 1) / wgs;
-    const int64_t least = p.shared ? 8 : 4;  // chunks per split worth a piece of its own
+    // Pieces to about 2048 workgroups (four rounds of the chip, which evens out
+    // ragged lengths), none where the tiles alone fill two.  Measured on
+    // MI355X with 8 cache heads of 128: 48 sequences to 16384 tokens 167 us
+    // (three pieces: 186), one of 65536 29 us (one piece per CU: 61 with
+    // pieces joined by one thread each), 128 of 2000 56 us (two pieces: 77).
+    // A piece is at least a chunk for each wave, two where there are more
+    // tiles: one sequence of 777 10.1 us (unsplit: 11.8), 8 of 4096 16.7 us
+    // (pieces of four chunks: 18.2), 64 of 500 12.6 us (23.5).
+    int64_t splits = wgs >= 1024 ? 1 : (2048 + wgs - 1) / wgs;
+    const int64_t least = wgs >= 64 ? 8 : 4;
     splits = splits < chunks / least ? splits : chunks / least;
+    splits = splits < 64 ? splits : 64;
     const int64_t piece = wgs * p.cols * (dim + 2);  // floats per split
     const int64_t cap = ((int64_t)256 << 20) / 4 / piece;
     splits = splits < cap ? splits : cap;

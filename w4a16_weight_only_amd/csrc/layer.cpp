@@ -96,12 +96,13 @@ int hip_status(hipError_t e, const char *what) {
 }
 
 // Host part of an attention call: the plan, or why there is none.
-int attention_plan(int64_t heads, const CacheArgs &c, int64_t max_pages, int64_t B, int64_t T, AttnPlan *plan) {
+int attention_plan(int64_t heads, const CacheArgs &c, int64_t max_pages, int64_t B, int64_t T, bool single,
+                   AttnPlan *plan) {
     if (heads <= 0 || heads % c.heads != 0)
         return fail(W4A16_ERR_INVALID_ARG, "query heads must be a positive multiple of the cache's heads");
     if (heads > 1024 || T * (heads / c.heads) >= ((int64_t)1 << 30))
         return fail(W4A16_ERR_UNSUPPORTED, "more than 1024 query heads, or too many rows for 32-bit indexing");
-    *plan = plan_attention(heads, c.heads, c.dim, (int64_t)1 << c.page_shift, max_pages, B, T);
+    *plan = plan_attention(heads, c.heads, c.dim, (int64_t)1 << c.page_shift, max_pages, B, T, single);
     if (plan->tiles * c.heads * plan->splits > kMaxGrid)
         return fail(W4A16_ERR_UNSUPPORTED, "too many rows and heads for one launch");
     return W4A16_OK;
@@ -231,9 +232,13 @@ size_t w4a16_attention_workspace_bytes(int64_t heads, const w4a16_kv_cache *cach
     CacheArgs c;
     AttnPlan plan;
     if (B <= 0 || T <= 0 || max_pages <= 0 || B > kMaxRows || T > kMaxRows || max_pages > ((int64_t)1 << 26) ||
-        check_cache(cache, &c) != W4A16_OK || attention_plan(heads, c, max_pages, B, T, &plan) != W4A16_OK)
+        check_cache(cache, &c) != W4A16_OK || attention_plan(heads, c, max_pages, B, T, false, &plan) != W4A16_OK)
         return 0;
-    return plan.part_floats * sizeof(float);
+    size_t floats = plan.part_floats;
+    // one row per sequence may come with or without offsets
+    if (T == B && attention_plan(heads, c, max_pages, B, T, true, &plan) == W4A16_OK)
+        floats = std::max(floats, plan.part_floats);
+    return floats * sizeof(float);
 }
 
 int w4a16_attention(const uint16_t *q, int64_t ldq, int64_t heads, const w4a16_kv_cache *cache,
@@ -252,7 +257,7 @@ int w4a16_attention(const uint16_t *q, int64_t ldq, int64_t heads, const w4a16_k
     if (T == 0) return ok();
     if (!q || !out) return fail(W4A16_ERR_INVALID_ARG, "q and out must be non-NULL when T > 0");
     if ((rc = check_sequences(c, block_table, max_pages, lens, rows, B, T, &s)) != W4A16_OK) return rc;
-    if ((rc = attention_plan(heads, c, max_pages, B, T, &plan)) != W4A16_OK) return rc;
+    if ((rc = attention_plan(heads, c, max_pages, B, T, !rows, &plan)) != W4A16_OK) return rc;
     const int64_t width = heads * c.dim;
     if (ldq < width || ldq % 8 != 0) return fail(W4A16_ERR_INVALID_ARG, "ldq must be a multiple of 8 covering heads * dim");
     if (ldq >= ((int64_t)1 << 31)) return fail(W4A16_ERR_UNSUPPORTED, "ldq of 2^31 or more");
@@ -281,9 +286,9 @@ size_t w4a16_decode_kv_workspace_bytes(int64_t M, const w4a16_linear *lin, int64
         CacheArgs c;
         AttnPlan plan;
         if (max_pages <= 0 || max_pages > ((int64_t)1 << 26) || check_cache(caches + l, &c) != W4A16_OK ||
-            lin[4 * l].K % c.dim != 0 || attention_plan(lin[4 * l].K / c.dim, c, max_pages, M, M, &plan) != W4A16_OK)
+            lin[4 * l].K % c.dim != 0 || attention_plan(lin[4 * l].K / c.dim, c, max_pages, M, M, true, &plan) != W4A16_OK)
             return 0;
-        attn = std::max(attn, plan.part_floats * sizeof(float));
+        attn = std::max(attn, w4a16_attention_workspace_bytes(lin[4 * l].K / c.dim, caches + l, max_pages, M, M));
     }
     return three + attn;
 }

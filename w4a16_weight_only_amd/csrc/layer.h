@@ -59,15 +59,16 @@ hipError_t launch_kv_append(const uint16_t *k, int64_t ldk, const uint16_t *v, i
 // chunks of the longest cache the table can hold.
 struct AttnPlan {
     int nt = 1;         // 16-column tiles per wave
-    bool shared = true; // the four waves share one column tile and divide its tokens
+    bool shared = true; // a workgroup's waves share one column tile and divide its tokens
     int cols = 16;      // columns per workgroup
     int64_t tiles = 0;  // column tiles per key/value head, an upper bound
     int splits = 1;
     int quota = 0;      // chunks per split
+    int join_cols = 16; // columns the pieces of a tile are joined for
     size_t part_floats = 0;  // workspace: partial outputs, then (max, sum) pairs
 };
 AttnPlan plan_attention(int64_t heads, int64_t kv_heads, int64_t dim, int64_t page, int64_t max_pages, int64_t B,
-                        int64_t T);
+                        int64_t T, bool single);
 hipError_t launch_attention(const uint16_t *q, int64_t ldq, int heads, const CacheArgs &c, const SeqArgs &s,
                             float scale, int64_t window, uint16_t *out, float *workspace, const AttnPlan &plan,
                             hipStream_t stream);
