@@ -776,10 +776,12 @@ AttnPlan plan_attention(int64_t heads, int64_t kv_heads, int64_t dim, int64_t pa
     // (three pieces: 186), one of 65536 29 us (one piece per CU: 61 with
     // pieces joined by one thread each), 128 of 2000 56 us (two pieces: 77).
     // A piece is at least a chunk for each wave, two where there are more
-    // tiles: one sequence of 777 10.1 us (unsplit: 11.8), 8 of 4096 16.7 us
-    // (pieces of four chunks: 18.2), 64 of 500 12.6 us (23.5).
+    // tiles: 4 of 2048 10.7 us (unsplit: 14.8), 8 of 4096 16.7 us (pieces of
+    // four chunks: 18.2), 64 of 500 12.6 us (23.5).  Up to 1024 tokens stay
+    // whole: the second launch costs what it saves (one of 777 10.1 us against
+    // 11.8 in a graph, 14.2 against 12 launched one by one).
     int64_t splits = wgs >= 1024 ? 1 : (2048 + wgs - 1) / wgs;
-    const int64_t least = wgs >= 64 ? 8 : 4;
+    const int64_t least = wgs >= 64 ? 8 : chunks <= 16 ? 16 : 4;
     splits = splits < chunks / least ? splits : chunks / least;
     splits = splits < 64 ? splits : 64;
     const int64_t piece = wgs * p.cols * (dim + 2);  // floats per split

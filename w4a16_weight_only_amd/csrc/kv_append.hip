@@ -16,7 +16,7 @@
 // order in which attention's matrix instructions take 16 bytes per lane.
 //
 // One workgroup owns one (page, head) of K or of V, so no two touch the same
-// scale: it reads the new rows for amax, again (from cache) to write codes.
+// scale: it reads the new rows for amax, again (from L2) to write codes.
 // Bound by HBM for prompts and by latency for single tokens.
 #include "device.h"
 #include "layer.h"
@@ -40,6 +40,8 @@ __device__ __forceinline__ float scaled(float x, float inv, bool top) {
 __device__ __forceinline__ float fp8_value(uint32_t code) {
     return __builtin_amdgcn_cvt_f32_fp8((int)code, 0);
 }
+
+constexpr int kTurn = 64;  // tokens transposed at a time
 
 template <int THREADS>
 __global__ __launch_bounds__(THREADS) void kv_append_kernel(const uint16_t *__restrict__ kin, int64_t ldk,
@@ -84,14 +86,33 @@ __global__ __launch_bounds__(THREADS) void kv_append_kernel(const uint16_t *__re
     uint8_t *codes = (is_v ? c.v : c.k) + slot * page * D;
     uint8_t *scale = (is_v ? c.v_scale : c.k_scale) + slot;
 
-    const int vpr = D >> 3;  // 16-byte vectors per row
+    // 16-byte vectors: vector i is columns 8 (i % vpr) of the page's new token
+    // i / vpr, vpr = D / 8 a power of two.  Up to four per thread (64 tokens of
+    // 128 dims) stay in registers between the two uses, else they are read
+    // again.
+    const int vshift = D == 64 ? 3 : D == 128 ? 4 : 5, vectors = m << vshift, vmask = (1 << vshift) - 1;
+    const bool hold = vectors <= 4 * THREADS && a + m <= (a & ~15) + kTurn;
+    auto load = [&](int i) {
+        return *reinterpret_cast<const u32x4 *>(in + (row + (i >> vshift)) * ld + 8 * (i & vmask));
+    };
     float amax = 0.f;
-    for (int i = threadIdx.x; i < m * vpr; i += THREADS) {
-        const int t = i / vpr, d = (i - t * vpr) * 8;
-        const u32x4 x = *reinterpret_cast<const u32x4 *>(in + (row + t) * ld + d);
+    auto largest = [&](const u32x4 &x) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             amax = fmaxf(amax, finite_abs(f16_bits_to_f32((x[e >> 1] >> (16 * (e & 1))) & 0xffffu)));
+    };
+    u32x4 held[4];
+    if (hold) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int i = threadIdx.x + k * THREADS;
+            held[k] = i < vectors ? load(i) : u32x4{0u, 0u, 0u, 0u};
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) largest(held[k]);
+    } else {
+#pragma unroll 4
+        for (int i = threadIdx.x; i < vectors; i += THREADS) largest(load(i));
     }
 #pragma unroll
     for (int o = 32; o; o >>= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
@@ -123,19 +144,75 @@ __global__ __launch_bounds__(THREADS) void kv_append_kernel(const uint16_t *__re
     const bool top = e == kKvMaxExp;
     if constexpr (THREADS > 64) __syncthreads();  // every thread has read the old scale
     if (threadIdx.x == 0) *scale = (uint8_t)(e + 127);
-    for (int i = threadIdx.x; i < m * vpr; i += THREADS) {
-        const int t = i / vpr, d = (i - t * vpr) * 8;
-        const u32x4 x = *reinterpret_cast<const u32x4 *>(in + (row + t) * ld + d);
+    auto codes_of = [&](const u32x4 &x) {
         float f[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] = scaled(f16_bits_to_f32((x[j >> 1] >> (16 * (j & 1))) & 0xffffu), inv, top);
-        const u32x2 o{pack_fp8x4(f[0], f[1], f[2], f[3]), pack_fp8x4(f[4], f[5], f[6], f[7])};
-        if (!is_v) {
-            *reinterpret_cast<u32x2 *>(codes + (size_t)(a + t) * D + d) = o;
-        } else {
+        return u32x2{pack_fp8x4(f[0], f[1], f[2], f[3]), pack_fp8x4(f[4], f[5], f[6], f[7])};
+    };
+    // put(i, codes) for vectors from .. to
+    auto each = [&](int from, int to, auto put) __attribute__((always_inline)) {
+        if (hold) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                codes[(size_t)(d + j) * page + a + t] = (uint8_t)(o[j >> 2] >> (8 * (j & 3)));
+            for (int k = 0; k < 4; ++k) {
+                const int i = threadIdx.x + k * THREADS;
+                if (i < vectors) put(i, codes_of(held[k]));
+            }
+        } else {
+            for (int i = from + threadIdx.x; i < to; i += THREADS) put(i, codes_of(load(i)));
+        }
+    };
+    if (!is_v) {
+        each(0, vectors, [&](int i, u32x2 o) { *reinterpret_cast<u32x2 *>(codes + (size_t)a * D + 8 * (size_t)i) = o; });
+    } else if constexpr (THREADS == 64) {
+        // one token: a byte of each dim's row
+        each(0, vectors, [&](int i, u32x2 o) {
+            const int t = i >> vshift, d = 8 * (i & vmask);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) codes[(size_t)(d + j) * page + a + t] = (uint8_t)(o[j >> 2] >> (8 * (j & 3)));
+        });
+    } else {
+        // Transposed through LDS, 64 tokens at a time: a thread turns 4 dims of
+        // 16 tokens (16 reads of 4 bytes) into 16 bytes of each dim's row.
+        __shared__ __align__(16) uint8_t tile[kTurn * (256 + 8)];
+        const int stride = D + 8, qshift = vshift + 1, quads = 1 << qshift;
+        for (int base = a & ~15; base < a + m; base += kTurn) {
+            const int first = base > a ? base : a, end = base + kTurn < a + m ? base + kTurn : a + m;
+            each((first - a) << vshift, (end - a) << vshift, [&](int i, u32x2 o) {
+                *reinterpret_cast<u32x2 *>(&tile[(a - base + (i >> vshift)) * stride + 8 * (i & vmask)]) = o;
+            });
+            __syncthreads();
+            for (int u = threadIdx.x; u < quads * ((end - base + 15) >> 4); u += THREADS) {
+                const int j = u >> qshift, d = (u & (quads - 1)) * 4, t0 = base + 16 * j;
+                uint32_t r[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) r[k] = *reinterpret_cast<const uint32_t *>(&tile[(16 * j + k) * stride + d]);
+                u32x4 o[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    // 4 tokens x 4 dims of bytes
+                    const uint32_t p0 = __builtin_amdgcn_perm(r[4 * k + 1], r[4 * k], 0x05010400u);
+                    const uint32_t p1 = __builtin_amdgcn_perm(r[4 * k + 3], r[4 * k + 2], 0x05010400u);
+                    const uint32_t q0 = __builtin_amdgcn_perm(r[4 * k + 1], r[4 * k], 0x07030602u);
+                    const uint32_t q1 = __builtin_amdgcn_perm(r[4 * k + 3], r[4 * k + 2], 0x07030602u);
+                    o[0][k] = __builtin_amdgcn_perm(p1, p0, 0x05040100u);
+                    o[1][k] = __builtin_amdgcn_perm(p1, p0, 0x07060302u);
+                    o[2][k] = __builtin_amdgcn_perm(q1, q0, 0x05040100u);
+                    o[3][k] = __builtin_amdgcn_perm(q1, q0, 0x07060302u);
+                }
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    uint8_t *dst = codes + (size_t)(d + x) * page + t0;
+                    if (t0 >= a && t0 + 16 <= a + m) {
+                        *reinterpret_cast<u32x4 *>(dst) = o[x];
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            if (t0 + k >= a && t0 + k < a + m) dst[k] = (uint8_t)(o[x][k >> 2] >> (8 * (k & 3)));
+                    }
+                }
+            }
+            __syncthreads();
         }
     }
 }
