@@ -323,7 +323,7 @@ typedef enum {
  *   y8, y8_scales  device e4m3 [M, K] and fp32 [M, ceil(K / 128)].
  * A block that holds an infinity or a NaN comes back with NaN in it.
  * Errors: as for w4a16_add_rmsnorm; UNSUPPORTED beyond one launch
- * (M * ceil(K / 2048) > 2^24).
+ * (M * ceil(K / 2048) > 2^23).
  */
 int w4a16_quant_fp8(int act, const uint16_t *x, int64_t ldx, int64_t M, int64_t K, uint8_t *y8, float *y8_scales,
                     hipStream_t stream);
@@ -346,7 +346,7 @@ int w4a16_quant_fp8(int act, const uint16_t *x, int64_t ldx, int64_t M, int64_t 
  * NaN codes and non-finite scales propagate to the outputs they enter.
  * Errors: INVALID_ARG for NULL pointers, sizes <= 0 (M < 0), overlap;
  * UNSUPPORTED for K % 16 != 0, pointers that are not 16-byte aligned (scales:
- * 4-byte), M > 2^20, K or N > 2^26, M * N past one launch (2^36); HIP on
+ * 4-byte), M > 2^20, K or N > 2^26, M * N past one launch (2^35); HIP on
  * launch failure.
  */
 int w4a16_gemm_fp8(const uint8_t *a, const float *a_scales, const uint8_t *b, const float *b_scales, int64_t M,
@@ -451,8 +451,8 @@ int w4a16_attention(const uint16_t *q, int64_t ldq, int64_t heads, const w4a16_k
  *                w4a16_gemm_glue(RMSNORM, R, H, gate_up)      -> P
  *                w4a16_gemm_glue(SWIGLU, P, 2I, down)         -> R
  *     then       w4a16_rownorm(R, H, M, H)                    -> x_out
- *   caches  host array of n_layers caches; block_table and lens (with this
- *           token) are shared by the layers.
+ *   caches  host array of n_layers caches, apart in memory; block_table and
+ *           lens (with this token) are shared by the layers.
  * Errors: as for w4a16_decode_step, w4a16_kv_append and w4a16_attention.
  */
 size_t w4a16_decode_kv_workspace_bytes(int64_t M, const w4a16_linear *lin, int64_t n_layers,

@@ -553,6 +553,44 @@ def test_attention_bad_pages_and_lengths_are_nan():
     check(got, want, bound, "bad pages")
 
 
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("counts", [[1, 1], [100, 90]])
+def test_attention_bad_pages_and_nan_in_whole_chunks(page, counts):
+    """The same far behind the rows, in chunks that every row of a tile sees whole."""
+    g = synth.rng(33)
+    H, group, D, n = 2, 2, 64, 700
+    q, c, table, lens, off = attention_case(g, [n, n], counts, H, group, D, page)
+    table[0, 70 // page] = -5
+    pid, slot = table[1, 200 // page], 200 % page
+    c["v"][pid, 0, 3, slot] = 0x7F
+    pid, slot = table[1, 330 // page], 330 % page
+    c["k"][pid, 1, slot, 9] = 0x7F
+    got, want, bound = run_attention(q, c, table, lens, off, D ** -0.5)
+    assert np.isnan(want[:counts[0]]).all() and 0 < np.isnan(want[counts[0]:]).mean() < 1
+    bound[np.isnan(bound)] = 1.0
+    check(got, want, bound, "whole chunks")
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with its own workspace from the allocator, give what they give alone."""
+    g = synth.rng(35)
+    jobs = []
+    for i in range(2):
+        q, c, table, lens, off = attention_case(g, [3000 + 500 * i, 700], [1, 1], 1, 4, 128, 64, width=80)
+        args = dev(q), cache_dev(c), dev(table), dev(lens)
+        jobs.append((args, host(w4.w4a16_attention(*args))))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    outs = [[] for _ in jobs]
+    for _ in range(20):
+        for s, (args, _), o in zip(streams, jobs, outs):
+            with torch.cuda.stream(s):
+                o.append(w4.w4a16_attention(*args))
+    torch.cuda.synchronize()
+    for (_, want), got in zip(jobs, outs):
+        assert all(np.array_equal(host(x), want) for x in got)
+
+
 def test_attention_infinite_query_is_nan():
     g = synth.rng(37)
     q, c, table, lens, off = attention_case(g, [30, 30], [1, 1], 1, 1, 64, 16)

@@ -78,6 +78,19 @@ def test_gemm_fp8_rejects(lib, kw, status):  # noqa: F811
     assert lib.w4a16_last_error().decode() != ""
 
 
+def test_gemm_fp8_plan(lib):  # noqa: F811
+    # few rows and long K: the row kernel; then tiles, divided along K where they are few
+    assert w4.w4a16_gemm_fp8_plan(1, 12800, 4096) == (16, 16, 8)
+    assert w4.w4a16_gemm_fp8_plan(64, 12800, 4096) == (32, 32, 4)
+    assert w4.w4a16_gemm_fp8_plan(256, 12800, 4096) == (64, 64, 2)
+    assert w4.w4a16_gemm_fp8_plan(4096, 4096, 25600) == (256, 256, 1)
+    assert w4.w4a16_gemm_fp8_plan(1 << 20, 1 << 23, 64) == (16, 16, 8)  # rows past the tiles' 32-bit offsets
+    for sizes, status in (((4, 264, 8), UNSUPPORTED), ((-1, 256, 8), INVALID), ((1 << 20, 256, 1 << 24), UNSUPPORTED)):
+        with pytest.raises(w4.W4A16Error) as e:
+            w4.w4a16_gemm_fp8_plan(*sizes)
+        assert e.value.status == status
+
+
 def test_gemm_fp8_noop(lib):  # noqa: F811
     assert gemm(lib, M=0, a=None, sa=None, out=None) == OK
     assert gemm(lib, M=0, b=None) == INVALID
@@ -179,6 +192,12 @@ def _caches(**kw):
     return cs
 
 
+def _same_cache_twice():
+    cs = _caches()
+    cs[1] = cs[0]
+    return cs
+
+
 def step(lib, stack=None, caches=None, tb=TB, mp=4, ln=LN, scale=0.1, x=X, y=Y, M=3, ws=WS, wsb=1 << 30, layers=2):  # noqa: F811
     s = ctypes.cast(stack if stack is not None else _stack(), ctypes.c_void_p)
     c = ctypes.cast(caches if caches is not None else _caches(), ctypes.c_void_p)
@@ -191,7 +210,7 @@ def step(lib, stack=None, caches=None, tb=TB, mp=4, ln=LN, scale=0.1, x=X, y=Y, 
     (dict(ln=None), INVALID), (dict(mp=0), INVALID), (dict(wsb=1000), INVALID), (dict(stack=_stack(KV=192)), INVALID),
     (dict(caches=_caches(page=24)), UNSUPPORTED), (dict(x=X + 2), UNSUPPORTED), (dict(ws=WS + 8), UNSUPPORTED),
     (dict(ws=X), INVALID), (dict(ws=KC), INVALID), (dict(y=VC), INVALID), (dict(y=X + 256), INVALID),
-    (dict(y=LN), INVALID),
+    (dict(y=LN), INVALID), (dict(caches=_same_cache_twice()), INVALID),
 ])
 def test_decode_step_kv_rejects(lib, kw, status):  # noqa: F811
     assert step(lib, **kw) == status

@@ -7,6 +7,8 @@
 #include <algorithm>
 #include <cmath>
 #include <string>
+#include <utility>
+#include <vector>
 
 #include "kernels.h"
 #include "layer.h"
@@ -51,7 +53,7 @@ Range rows_range(const void *p, int64_t rows, int64_t ld, int64_t width) {
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 constexpr int64_t kMaxRows = (int64_t)1 << 20;  // as for w4a16_gemm
-constexpr int64_t kMaxGrid = (int64_t)1 << 24;  // workgroups of 256 threads in one launch
+constexpr int64_t kMaxGrid = (int64_t)1 << 23;  // workgroups of 256 threads in one launch (2^32 threads at most)
 
 int check_cache(const w4a16_kv_cache *c, CacheArgs *out) {
     if (!c) return fail(W4A16_ERR_INVALID_ARG, "cache must be non-NULL");
@@ -326,15 +328,22 @@ int w4a16_decode_step_kv(const w4a16_linear *lin, int64_t n_layers, const w4a16_
     if (!aligned16(x_in) || !aligned16(x_out) || !aligned16(workspace))
         return fail(W4A16_ERR_UNSUPPORTED, "x_in, x_out and workspace must be 16-byte aligned");
     const Range x{x_in, (size_t)M * H * 2}, y{x_out, (size_t)M * H * 2}, ws{workspace, need};
+    std::vector<std::pair<uintptr_t, uintptr_t>> spans;  // the caches' arrays
+    spans.reserve(4 * n_layers);
     bool bad = overlaps(ws, x) || overlaps(ws, y) || (x_in != x_out && overlaps(x, y)) ||
                overlaps(y, Range{block_table, (size_t)M * max_pages * 4}) || overlaps(y, Range{lens, (size_t)M * 4});
     for (int64_t l = 0; l < n_layers; ++l) {
         const w4a16_kv_cache &k = caches[l];
         const size_t n = (size_t)k.pages * k.heads * k.page * k.dim, ns = (size_t)k.pages * k.heads;
         const Range parts[4] = {{k.k, n}, {k.v, n}, {k.k_scale, ns}, {k.v_scale, ns}};
-        for (const Range &r : parts) bad = bad || overlaps(r, ws) || overlaps(r, x) || overlaps(r, y);
+        for (const Range &r : parts) {
+            bad = bad || overlaps(r, ws) || overlaps(r, x) || overlaps(r, y);
+            spans.emplace_back(reinterpret_cast<uintptr_t>(r.p), reinterpret_cast<uintptr_t>(r.p) + r.n);
+        }
     }
-    if (bad) return fail(W4A16_ERR_INVALID_ARG, "x_in, x_out, workspace and the caches must not overlap (x_out may be x_in)");
+    std::sort(spans.begin(), spans.end());
+    for (size_t i = 1; i < spans.size(); ++i) bad = bad || spans[i].first < spans[i - 1].second;
+    if (bad) return fail(W4A16_ERR_INVALID_ARG, "x_in, x_out, workspace and the layers' caches must not overlap (x_out may be x_in)");
     // Buffers: P the linears' wide outputs, Q attention and glue scratch, R the
     // hidden rows between the linears.
     const size_t buf = three / 3;
