@@ -456,6 +456,29 @@ def test_attention(case, window):
         check(got1, want1, np.where(bound1 == 0, 1e-30, bound1), "single rows")
 
 
+@pytest.mark.parametrize("D,page,window", [(64, 16, 0), (64, 64, 60), (128, 64, 0), (128, 16, 60), (128, 256, 0)])
+def test_attention_many_tiles(D, page, window):
+    """Enough workgroups for the kernel that holds two column tiles per wave: many heads, of which some are compared; one
+    sequence has a page out of range and NaN among its values."""
+    H, group, lens, counts = 128, 2, [150, 330, 190], [150, 70, 190]
+    g = synth.rng(D + page)
+    q, c, table, lens, off = attention_case(g, lens, counts, H, group, D, page, extra_rows=1)
+    table[2, 100 // page] = -3
+    pid, slot = table[1, 20 // page], 20 % page
+    c["v"][pid, 5, 7, slot] = 0x7F
+    out = torch.full(q.shape, -77.0, dtype=torch.float16, device="cuda")
+    w4.w4a16_attention(dev(q), cache_dev(c), dev(table), dev(lens), dev(off), window=window, out=out)
+    out = host(out)
+    assert (out[-1] == -77).all()
+    for h in (0, 5, 70, 127):
+        sub = {n: x[:, h:h + 1] for n, x in c.items()}
+        cols = slice(h * group * D, (h + 1) * group * D)
+        want = np.full((q.shape[0], group * D), -77.0)
+        bound = lo.attention(q[:, cols], sub, table, lens, off, D ** -0.5, window, want)
+        bound[np.isnan(bound)] = 1.0
+        check(out[:, cols], want, np.where(bound == 0, 1e-30, bound), "head %d" % h)
+
+
 @pytest.mark.parametrize("lens,counts,H,group,D,page,width", [
     ([5000, 64, 1, 3000, 0], [1] * 5, 1, 4, 128, 64, 200), ([2500, 130], [1, 1], 1, 16, 64, 16, 300),
     ([3000], [9], 1, 8, 128, 32, 120), ([1200, 700], [40, 30], 1, 2, 128, 64, 60), ([900], [1], 1, 6, 256, 128, 16)])

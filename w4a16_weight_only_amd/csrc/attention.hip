@@ -762,7 +762,12 @@ AttnPlan plan_attention(int64_t heads, int64_t kv_heads, int64_t dim, int64_t pa
     const int64_t group = heads / kv_heads;
     const int64_t per = (T * group + B - 1) / B;  // columns of the average sequence
     p.shared = per <= 16;
-    p.nt = p.shared || per <= 64 || dim == 256 ? 1 : 2;
+    // Two column tiles per wave share each conversion of keys and values; one
+    // gives twice the workgroups.  Measured on MI355X: 2000 rows after 6000
+    // tokens (504 workgroups with two) 271 us, 337 with one; 1000 rows (256)
+    // 35 us, 29 with one.
+    p.nt = 1;
+    if (!p.shared && per > 64 && dim < 256 && (T * group / 128 + B) * kv_heads >= 400) p.nt = 2;
     p.cols = p.shared ? 16 : 64 * p.nt;
     // ragged rows: an upper bound, sequence b's tiles beginning at
     // floor(rows[b] * group / cols) + b
@@ -770,18 +775,28 @@ AttnPlan plan_attention(int64_t heads, int64_t kv_heads, int64_t dim, int64_t pa
     p.join_cols = (int)(single && group < p.cols ? group : p.cols);
     const int64_t chunks = (max_pages * page + kChunk - 1) / kChunk;
     const int64_t wgs = p.tiles * kv_heads;
-    // Pieces to about 2048 workgroups (four rounds of the chip, which evens out
-    // ragged lengths), none where the tiles alone fill two.  Measured on
-    // MI355X with 8 cache heads of 128: 48 sequences to 16384 tokens 167 us
-    // (three pieces: 186), one of 65536 29 us (one piece per CU: 61 with
-    // pieces joined by one thread each), 128 of 2000 56 us (two pieces: 77).
-    // A piece is at least a chunk for each wave, two where there are more
-    // tiles: 4 of 2048 10.7 us (unsplit: 14.8), 8 of 4096 16.7 us (pieces of
-    // four chunks: 18.2), 64 of 500 12.6 us (23.5).  Up to 1024 tokens stay
-    // whole: the second launch costs what it saves (one of 777 10.1 us against
-    // 11.8 in a graph, 14.2 against 12 launched one by one).
-    int64_t splits = wgs >= 1024 ? 1 : (2048 + wgs - 1) / wgs;
-    const int64_t least = wgs >= 64 ? 8 : chunks <= 16 ? 16 : 4;
+    int64_t splits, least;
+    if (p.shared) {
+        // Pieces to about 2048 workgroups (four rounds of the chip, which evens
+        // out ragged lengths), none where the tiles alone fill two.  Measured
+        // on MI355X with 8 cache heads of 128: 48 sequences to 16384 tokens
+        // 167 us (three pieces: 186), one of 65536 29 us, 128 of 2000 56 us
+        // (two pieces: 77).  A piece is at least a chunk for each wave, two
+        // where there are more tiles: 4 of 2048 10.7 us (unsplit: 14.8), 8 of
+        // 4096 16.7 us (pieces of four chunks: 18.2), 64 of 500 12.6 us
+        // (23.5).  Up to 1024 tokens stay whole: the second launch costs what
+        // it saves (one of 777 10.1 us against 11.8 in a graph, 14.2 against
+        // 12 launched one by one).
+        splits = wgs >= 1024 ? 1 : (2048 + wgs - 1) / wgs;
+        least = wgs >= 64 ? 8 : chunks <= 16 ? 16 : 4;
+    } else {
+        // A piece of a prompt writes and reads back far more than it saves
+        // once the tiles come near to filling the chip: 1000 rows (264
+        // workgroups) 29 us whole, 80 in two pieces; 128 rows after 3872
+        // tokens (72) 33 us in seven pieces, 74 whole.
+        splits = wgs >= 192 ? 1 : (512 + wgs - 1) / wgs;
+        least = 8;
+    }
     splits = splits < chunks / least ? splits : chunks / least;
     splits = splits < 64 ? splits : 64;
     const int64_t piece = wgs * p.cols * (dim + 2);  // floats per split
