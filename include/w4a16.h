@@ -422,8 +422,9 @@ int w4a16_kv_append(const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t l
  *   workspace  device scratch of w4a16_attention_workspace_bytes() bytes
  *          (NULL where that is 0), caller-owned, not shared with a call that
  *          may run at the same time; nothing in it need be initialised.
- * Scores and softmax are fp32; the weights are rounded to fp16 for the product
- * with the values.  The order of the sums depends on the sizes alone (B, T,
+ * Scores and softmax are fp32; for the product with the values the weights are
+ * rounded to fp16 where a sequence has many rows and heads, and carried as two
+ * fp16 values where it has few (single tokens).  The order of the sums depends on the sizes alone (B, T,
  * max_pages) and lens, so results repeat bit for bit.
  * Errors: as for w4a16_kv_append; INVALID_ARG also for heads that are no
  * multiple of the cache's, a scale that is not finite, window < 0, a short

@@ -17,9 +17,11 @@
 // lane dequantises them: to fp16, exactly (kv_append.hip).
 //
 // Rounding: q and k are exact in fp16, their products summed in fp32; the
-// softmax runs in fp32; P is rounded once to fp16 for the second product
-// (2^-12 of each weight at most, against 2^-12 of the result's own rounding),
-// the sums of P stay unrounded in fp32, and so does O until the output.
+// softmax runs in fp32.  For the second product prompts round P once to fp16
+// (2^-11 of each weight at most, as large as the result's own rounding; the
+// sums take the rounded weights too), at the rate of the matrix cores; single
+// tokens, bound by reading the cache, carry each weight as two fp16 values.
+// O and the sums of P are fp32 until the output.
 //
 // The maximum a column's weights are taken against is raised only when some
 // score passes it by 2^8 (weights then stay below 2^8, far inside fp16), so
@@ -153,8 +155,11 @@ struct Pages {
 
 // NT tiles of 16 columns held by one wave: queries, running maxima, the sums of
 // the weights (one more row of O, from values of one) and O, all of it fp32.
-template <int D, int NT>
+// FINE: weights enter the second product as two fp16 values, the second what
+// the first left over, so they are good to 2^-22.
+template <int D, int NT, bool FINE>
 struct Columns {
+    static constexpr int PARTS = FINE ? 2 : 1;
     static constexpr int KD = D / 64;  // 16-byte key pieces per lane and 16-token tile
     static constexpr int DT = D / 16;  // output tiles along dim
 
@@ -253,9 +258,9 @@ struct Columns {
                 }
     }
 
-    // Weights of a chunk, rounded to fp16.  The running maxima are raised when
+    // Weights of a chunk, as fp16.  The running maxima are raised when
     // a score passes them by kLazy after its scale.
-    __device__ __forceinline__ void weights(const f32x4 (&sc)[NT][4], f16x8 (&pf)[NT][2]) {
+    __device__ __forceinline__ void weights(const f32x4 (&sc)[NT][4], f16x8 (&pf)[NT][PARTS][2]) {
         float top[NT];
         bool raise = false;
 #pragma unroll
@@ -289,9 +294,12 @@ struct Columns {
 #pragma unroll
             for (int x = 0; x < 4; ++x)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    pf[n][x >> 1][4 * (x & 1) + i] =
-                        (f16)__builtin_amdgcn_exp2f(__builtin_fmaf(sc[n][x][i], scale, -base));
+                for (int i = 0; i < 4; ++i) {
+                    const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[n][x][i], scale, -base));
+                    const f16 h = (f16)e;
+                    pf[n][0][x >> 1][4 * (x & 1) + i] = h;
+                    if constexpr (FINE) pf[n][1][x >> 1][4 * (x & 1) + i] = (f16)(e - (float)h);
+                }
         }
     }
 
@@ -302,15 +310,18 @@ struct Columns {
     // overflow at the new scale), and NaN codes are taken out and put back only
     // for the columns that see them: those for which a product of ones counts.
     template <bool CLEAN, typename Value>
-    __device__ __forceinline__ void values(const f32x4 (&sc)[NT][4], const f16x8 (&pf)[NT][2], Value value, float fv,
+    __device__ __forceinline__ void values(const f32x4 (&sc)[NT][4], const f16x8 (&pf)[NT][PARTS][2], Value value, float fv,
                                            int left) {
         f16x8 ones;
 #pragma unroll
         for (int j = 0; j < 8; ++j) ones[j] = (f16)1;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            l[n] = mfma16(ones, pf[n][0], l[n]);
-            l[n] = mfma16(ones, pf[n][1], l[n]);
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q) {
+                l[n] = mfma16(ones, pf[n][q][0], l[n]);
+                l[n] = mfma16(ones, pf[n][q][1], l[n]);
+            }
         }
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
@@ -348,8 +359,11 @@ struct Columns {
             const f16x8 a0 = dequant8(v[0], v[1], fv), a1 = dequant8(v[2], v[3], fv);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                o[n][d] = mfma16(a0, pf[n][0], o[n][d]);
-                o[n][d] = mfma16(a1, pf[n][1], o[n][d]);
+#pragma unroll
+                for (int q = 0; q < PARTS; ++q) {
+                    o[n][d] = mfma16(a0, pf[n][q][0], o[n][d]);
+                    o[n][d] = mfma16(a1, pf[n][q][1], o[n][d]);
+                }
             }
         }
     }
@@ -366,7 +380,7 @@ struct Columns {
     template <bool CLEAN, typename Key, typename Value>
     __device__ __forceinline__ void chunk(int c, Key key, float fk, Value value, float fv, int page_v) {
         f32x4 sc[NT][4];
-        f16x8 pf[NT][2];
+        f16x8 pf[NT][PARTS][2];
         // matrix instructions first: the other wave of the SIMD does its softmax
         // meanwhile (prompts 627 -> 619 us)
         __builtin_amdgcn_s_setprio(1);
@@ -424,7 +438,7 @@ __global__ __launch_bounds__(256, (D == 64 ? 3 : D == 128 ? 2 : 1)) void attenti
     int chi = t.hi > t.lo ? (t.hi + kChunk - 1) / kChunk : clo;
     chi = chi < clo + p.quota ? chi : clo + p.quota;
 
-    Columns<D, 1> cs;
+    Columns<D, 1, true> cs;
     cs.init(p, t, at.kvh, t.c0);
     const Pages pages(p, t, at.kvh);
     const size_t page_bytes = (size_t)D << p.c.page_shift;
@@ -465,7 +479,7 @@ __global__ __launch_bounds__(256, (D == 64 ? 3 : D == 128 ? 2 : 1)) void attenti
         const int page_v = pv;
         if constexpr (decltype(clean)::value) lost = lost || __any(pk == -2 || pv == -2);
         f32x4 sc[1][4];
-        f16x8 pf[1][2];
+        f16x8 pf[1][2][2];
         cs.scores(sc, [&](int x, int m) { return kr[x][m]; }, scale_of((uint8_t)bk));
         if (more) {
             load_keys(c + W, pk_next);
@@ -567,7 +581,7 @@ __global__ __launch_bounds__(256, (D <= 128 ? 2 : 1)) void attention_rows_kernel
     // this wave's columns, and the chunks that any of them sees
     const int wc0 = t.c0 + wave * 16 * NT;
     const bool any_col = wc0 < t.ncols;
-    Columns<D, NT> cs;
+    Columns<D, NT, false> cs;
     cs.init(p, t, at.kvh, any_col ? wc0 : t.c0);
     const int own_hi = !any_col || cs.pos_max < 0 ? 0 : cs.pos_max / kChunk + 1;
     const int first_tok = p.window ? cs.pos_min - p.window + 1 : 0;
