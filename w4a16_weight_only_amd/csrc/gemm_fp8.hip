@@ -41,8 +41,8 @@ __device__ __forceinline__ i32x8 load_block(const uint8_t *row, int k0, int g, i
     return join(lo, hi);
 }
 
-__device__ __forceinline__ void store4(uint16_t *out, int64_t m, int n, int N, bool wide, const f32x4 &v) {
-    uint16_t *p = out + m * N + n;
+__device__ __forceinline__ void store4(uint16_t *out, int64_t m, int64_t ldo, int n, int N, bool wide, const f32x4 &v) {
+    uint16_t *p = out + m * ldo + n;
     if (wide && n + 4 <= N) {
         u32x2 w;
 #pragma unroll
@@ -64,7 +64,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void gemm_fp8_row_kernel(const uint
                                                                        const float *__restrict__ sa,
                                                                        const uint8_t *__restrict__ b,
                                                                        const float *__restrict__ sb, int M, int K, int N,
-                                                                       uint16_t *__restrict__ out) {
+                                                                       uint16_t *__restrict__ out, int64_t ldo) {
     __shared__ f32x4 sh[kRowWaves][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
     const int n0 = blockIdx.x * 16, m = blockIdx.y * 16 + r;
@@ -87,7 +87,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void gemm_fp8_row_kernel(const uint
     for (int w = 1; w < kRowWaves; ++w)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[j] += sh[w][lane][j];
-    store4(out, m, n0 + 4 * g, N, (N & 3) == 0, acc);
+    store4(out, m, ldo, n0 + 4 * g, N, (ldo & 3) == 0, acc);
 }
 
 // Direct loads into LDS, 16 or 4 bytes per lane: from the buffer at voff + soff
@@ -129,7 +129,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void gemm_fp8_tile_kernel(const 
                                                                       const uint8_t *__restrict__ b,
                                                                       const float *__restrict__ sb, int M, int K, int N,
                                                                       int tiles_m, int tiles_n,
-                                                                      uint16_t *__restrict__ out) {
+                                                                      uint16_t *__restrict__ out, int64_t ldo) {
     constexpr int W = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
     constexpr int kLoadB = BN / 8 / W, kLoadA = BM / 8 / W;  // direct loads per wave and step, and one of scales
     constexpr int kStage = (BM + BN) * kFp8Block;
@@ -301,27 +301,27 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void gemm_fp8_tile_kernel(const 
                     for (int x = 0; x < 4; ++x) acc[i][j][x] += v[x];
                 }
     }
-    const bool wide = (N & 3) == 0;
+    const bool wide = (ldo & 3) == 0;
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
         const int m = m0 + (wm * TM + j) * 16 + r;
         if (m >= M) continue;
 #pragma unroll
-        for (int i = 0; i < TN; ++i) store4(out, m, nrow + 16 * i + 4 * g, N, wide, acc[i][j]);
+        for (int i = 0; i < TN; ++i) store4(out, m, ldo, nrow + 16 * i + 4 * g, N, wide, acc[i][j]);
     }
 }
 
 
 template <int BM, int BN, int WM, int WN, int S, int KG>
 void launch_tile(const uint8_t *a, const float *sa, const uint8_t *b, const float *sb, int64_t M, int64_t K, int64_t N,
-                 uint16_t *out, hipStream_t stream) {
+                 uint16_t *out, int64_t ldo, hipStream_t stream) {
     const int tm = (int)((M + BM - 1) / BM), tn = (int)((N + BN - 1) / BN);
     gemm_fp8_tile_kernel<BM, BN, WM, WN, S, KG><<<dim3((unsigned)((tm * tn + 7) / 8 * 8)), dim3(64 * WM * WN * KG), 0, stream>>>(
-        a, sa, b, sb, (int)M, (int)K, (int)N, tm, tn, out);
+        a, sa, b, sb, (int)M, (int)K, (int)N, tm, tn, out, ldo);
 }
 
 typedef void (*TileLauncher)(const uint8_t *, const float *, const uint8_t *, const float *, int64_t, int64_t, int64_t,
-                             uint16_t *, hipStream_t);
+                             uint16_t *, int64_t, hipStream_t);
 
 // The tile shapes, with the time of one step (us, measured on MI355X) where a
 // CU holds one, two, .. of their workgroups; as many as its LDS and registers
@@ -344,39 +344,76 @@ const TileShape kShapes[] = {
     {256, 256, 1, 1, {2.0f}, launch_tile<256, 256, 2, 4, 2, 1>},
 };
 
-// The shape with the least estimated time: the busiest CU's rounds of
-// workgroups times the steps of one, not below the time of reading the
+constexpr double kReadRate = 4.7e6;  // bytes a us
+
+// Estimated time (us) of a shape: the busiest CU's rounds of workgroups times
+// the steps of one.
+double estimate(const TileShape &s, int64_t M, int64_t K, int64_t N) {
+    const int64_t nb = (K + kFp8Block - 1) / kFp8Block;
+    const int64_t tiles = ((M + s.bm - 1) / s.bm) * ((N + s.bn - 1) / s.bn), per_cu = (tiles + 255) / 256;
+    const int64_t full = per_cu / s.resident, rest = per_cu % s.resident;
+    return (double)((nb + s.groups - 1) / s.groups) *
+           ((double)full * s.step[s.resident - 1] + (rest ? s.step[rest - 1] : 0.0));
+}
+
+// The shape with the least estimated time, not below the time of reading the
 // operands.  Measured against all shapes at M = 1 .. 4096 of 4096 x 6144,
 // 4096 x 25600 and 12800 x 4096 the choice is within 10% of the best (e.g.
 // M = 64 12800 x 4096: 16 us, where the 128 x 128 tiles that win at M = 1024
 // take 66).  -1: the row kernel, whose step grows with the rows it reads.
-int choose(int64_t M, int64_t K, int64_t N) {
+int choose(int64_t M, int64_t K, int64_t N, double *us) {
     const int64_t nb = (K + kFp8Block - 1) / kFp8Block;
+    *us = 0;
     if (K > kTileMaxK) return -1;
-    const double least = (double)K * (double)(N + M) / 4.7e6;  // us at 4.7 TB/s
-    auto floor_at = [&](double us) { return us < least ? least : us; };
+    const double least = (double)K * (double)(N + M) / kReadRate;
     int best = -1;
     double t = 1e30;
-    if (M <= 16) t = floor_at((double)((N + 4095) / 4096) * (double)((nb + 7) / 8) * (.75 + .022 * (double)M));
+    if (M <= 16) {
+        *us = (double)((N + 4095) / 4096) * (double)((nb + 7) / 8) * (.75 + .022 * (double)M);
+        t = *us < least ? least : *us;
+    }
     for (int i = 0; i < (int)(sizeof(kShapes) / sizeof(kShapes[0])); ++i) {
-        const TileShape &s = kShapes[i];
-        const int64_t tiles = ((M + s.bm - 1) / s.bm) * ((N + s.bn - 1) / s.bn), per_cu = (tiles + 255) / 256;
-        const int64_t full = per_cu / s.resident, rest = per_cu % s.resident;
-        const double steps = (double)((nb + s.groups - 1) / s.groups);
-        const double us = steps * ((double)full * s.step[s.resident - 1] + (rest ? s.step[rest - 1] : 0.0));
-        const double score = floor_at(us) + .15 * us;  // among shapes at the floor, the one with time to spare
+        const double e = estimate(kShapes[i], M, K, N);
+        const double score = (e < least ? least : e) + .15 * e;  // among shapes at the floor, the one with time to spare
         if (score < t) {
             t = score;
             best = i;
+            *us = e;
         }
     }
     return best;
 }
 
+// Columns of the first of two launches: where the largest tiles' last round
+// would leave most CUs idle, the columns of the whole rounds come first and the
+// rest takes the shape of its own size.  N: one launch.  Measured with K = 4096
+// N = 25600: M = 4096 (6.25 rounds) 510 -> 500 us, M = 2048 (3.1 rounds) 314 ->
+// 283 us; less than the rounds saved, as fewer busy CUs run at higher clocks.
+int64_t first_columns(int64_t M, int64_t K, int64_t N, int shape, double us) {
+    const TileShape &s = kShapes[sizeof(kShapes) / sizeof(kShapes[0]) - 1];
+    if (shape != (int)(sizeof(kShapes) / sizeof(kShapes[0])) - 1) return N;
+    const int64_t tm = (M + s.bm - 1) / s.bm, tn = (N + s.bn - 1) / s.bn;
+    const int64_t n1 = tm * tn / 256 * 256 / tm * s.bn;
+    if (n1 <= 0 || n1 >= N) return N;
+    double rest;
+    choose(M, K, N - n1, &rest);
+    return estimate(s, M, K, n1) + rest + 4.0 < .94 * us ? n1 : N;  // a launch and its drain: about 4 us
+}
+
+void launch_one(int shape, const uint8_t *a, const float *sa, const uint8_t *b, const float *sb, int64_t M, int64_t K,
+                int64_t N, uint16_t *out, int64_t ldo, hipStream_t stream) {
+    if (shape < 0)
+        gemm_fp8_row_kernel<<<dim3((unsigned)((N + 15) / 16), (unsigned)((M + 15) / 16)), dim3(64 * kRowWaves), 0, stream>>>(
+            a, sa, b, sb, (int)M, (int)K, (int)N, out, ldo);
+    else
+        kShapes[shape].launch(a, sa, b, sb, M, K, N, out, ldo, stream);
+}
+
 }  // namespace
 
 void gemm_fp8_plan(int64_t M, int64_t K, int64_t N, int32_t *rows, int32_t *cols, int32_t *groups) {
-    const int i = choose(M, K, N);
+    double us;
+    const int i = choose(M, K, N, &us);
     *rows = i < 0 ? 16 : kShapes[i].bm;
     *cols = i < 0 ? 16 : kShapes[i].bn;
     *groups = i < 0 ? kRowWaves : kShapes[i].groups;
@@ -384,12 +421,15 @@ void gemm_fp8_plan(int64_t M, int64_t K, int64_t N, int32_t *rows, int32_t *cols
 
 hipError_t launch_gemm_fp8(const uint8_t *a, const float *sa, const uint8_t *b, const float *sb, int64_t M, int64_t K,
                            int64_t N, uint16_t *out, hipStream_t stream) {
-    const int i = choose(M, K, N);
-    if (i < 0)
-        gemm_fp8_row_kernel<<<dim3((unsigned)((N + 15) / 16), (unsigned)((M + 15) / 16)), dim3(64 * kRowWaves), 0, stream>>>(
-            a, sa, b, sb, (int)M, (int)K, (int)N, out);
-    else
-        kShapes[i].launch(a, sa, b, sb, M, K, N, out, stream);
+    double us;
+    const int i = choose(M, K, N, &us);
+    const int64_t n1 = first_columns(M, K, N, i, us);
+    launch_one(i, a, sa, b, sb, M, K, n1, out, N, stream);
+    if (n1 < N) {
+        const int64_t nb = (K + kFp8Block - 1) / kFp8Block;
+        const int j = choose(M, K, N - n1, &us);
+        launch_one(j, a, sa, b + n1 * K, sb + n1 / kFp8Block * nb, M, K, N - n1, out + n1, N, stream);
+    }
     return hipGetLastError();
 }
 
