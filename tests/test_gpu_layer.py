@@ -247,6 +247,18 @@ def test_gemm_fp8_exact_integers(M, K, N):
     assert np.array_equal(host(w4.w4a16_gemm_fp8(codes_dev(a), dev(sa), codes_dev(b), dev(sb))), want.astype(np.float16))
 
 
+def test_gemm_fp8_rows_past_the_tiles_offsets():
+    """K above 2^22, where every M takes the row kernel."""
+    M, K, N = 20, (1 << 22) + 16, 40
+    assert w4.w4a16_gemm_fp8_plan(M, K, N) == (16, 16, 8)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    a, b = ((torch.rand(r, K, generator=gen, device="cuda") < 0.01).to(FP8) for r in (M, N))
+    ones = (torch.ones(r, lo.blocks(K), device="cuda") for r in (M, 1))
+    sa, sb = ones
+    want = a.double() @ b.double().t().contiguous()          # counts of about 400: exact in fp16
+    assert np.array_equal(host(w4.w4a16_gemm_fp8(a, sa, b, sb)), host(want.half()))
+
+
 @pytest.mark.parametrize("M", [2, 40, 260])
 def test_gemm_fp8_nan_stays_in_its_row_and_column(M):
     K, N = 256, 272
@@ -641,6 +653,24 @@ def test_attention_malformed_offsets_stay_in_bounds():
     w4.w4a16_attention(qd, cd, dev(table), dev(lens), dev(np.array([20, 20, 40, 60], np.int32)), scale=0.125, out=late)
     late = host(late)
     assert (late[:20] == -77).all() and np.abs(late[20:] - want[20:]).max() < 0.01
+
+
+def test_cache_past_4_gib():
+    """Pages whose bytes lie past 32-bit offsets: the same results as from a small pool."""
+    H, D, page, n = 1, 128, 64, 200
+    g = synth.rng(47)
+    pages = 600_000                                           # 4.9 GB of keys, as much of values
+    k, v = synth.activations(g, n, D), synth.activations(g, n, D)
+    lens, rows = dev(np.array([n], np.int32)), dev(np.array([0, n], np.int32))
+    outs = []
+    for pool, ids in ((pages, [599_999, 3, 524_288, 524_289]), (5, [4, 3, 0, 1])):
+        c = w4.w4a16_kv_cache(pool, H, page, D)
+        table = dev(np.array([ids], np.int32))
+        w4.w4a16_kv_append(dev(k), dev(v), c, table, lens, rows)
+        q = dev(synth.activations(synth.rng(48), n, 4 * D))
+        outs.append((host(w4.w4a16_attention(q, c, table, lens, rows)), host(w4.w4a16_attention(q[-1:], c, table, lens)),
+                     host(c["k"][ids].contiguous()), host(c["v_scale"][ids].contiguous())))
+    assert all(np.array_equal(a, b) for a, b in zip(*outs)) and np.abs(outs[0][0]).max() > 0
 
 
 def test_attention_results_repeat():
