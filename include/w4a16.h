@@ -424,8 +424,8 @@ int w4a16_kv_append(const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t l
  *          may run at the same time; nothing in it need be initialised.
  * Scores and softmax are fp32; for the product with the values the weights are
  * rounded to fp16 where a sequence has many rows and heads, and carried as two
- * fp16 values where it has few (single tokens).  The order of the sums depends on the sizes alone (B, T,
- * max_pages) and lens, so results repeat bit for bit.
+ * fp16 values where it has few (single tokens).  The order of the sums depends
+ * on the sizes (B, T, max_pages) and lens alone, so results repeat bit for bit.
  * Errors: as for w4a16_kv_append; INVALID_ARG also for heads that are no
  * multiple of the cache's, a scale that is not finite, window < 0, a short
  * workspace, or out or workspace overlapping anything else; UNSUPPORTED for
@@ -453,7 +453,8 @@ int w4a16_attention(const uint16_t *q, int64_t ldq, int64_t heads, const w4a16_k
  *                w4a16_gemm_glue(SWIGLU, P, 2I, down)         -> R
  *     then       w4a16_rownorm(R, H, M, H)                    -> x_out
  *   caches  host array of n_layers caches, apart in memory; block_table and
- *           lens (with this token) are shared by the layers.
+ *           lens (with this token) are shared by the layers and lie outside
+ *           the caches and the workspace.
  * Errors: as for w4a16_decode_step, w4a16_kv_append and w4a16_attention.
  */
 size_t w4a16_decode_kv_workspace_bytes(int64_t M, const w4a16_linear *lin, int64_t n_layers,

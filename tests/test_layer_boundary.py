@@ -211,6 +211,7 @@ def step(lib, stack=None, caches=None, tb=TB, mp=4, ln=LN, scale=0.1, x=X, y=Y, 
     (dict(caches=_caches(page=24)), UNSUPPORTED), (dict(x=X + 2), UNSUPPORTED), (dict(ws=WS + 8), UNSUPPORTED),
     (dict(ws=X), INVALID), (dict(ws=KC), INVALID), (dict(y=VC), INVALID), (dict(y=X + 256), INVALID),
     (dict(y=LN), INVALID), (dict(caches=_same_cache_twice()), INVALID),
+    (dict(tb=WS), INVALID), (dict(ln=WS), INVALID), (dict(tb=KC), INVALID), (dict(ln=KS), INVALID),
 ])
 def test_decode_step_kv_rejects(lib, kw, status):  # noqa: F811
     assert step(lib, **kw) == status
@@ -241,3 +242,7 @@ def test_python_binding_refuses(lib):  # noqa: F811
     assert c["k"].shape == (2, 1, 16, 64) and c["v"].shape == (2, 1, 64, 16) and int(c["k_scale"][0, 0]) == 112
     with pytest.raises(ValueError, match="GPU"):
         w4.w4a16_kv_append(x, x, c, None, None)
+    # elements between a strided workspace's own would be overwritten
+    assert w4._scratch(None) == (None, 0) and w4._scratch(x)[1] == 1024
+    with pytest.raises(ValueError, match="contiguous"):
+        w4._scratch(x[:, ::2])

@@ -388,6 +388,15 @@ def _same_device(first, *others):
             raise ValueError("a tensor is on %s, not on %s like the first" % (t.device, first.device))
 
 
+def _scratch(workspace):
+    """(pointer, bytes) of a caller's workspace, or of none."""
+    if workspace is None:
+        return None, 0
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 def _launch(first, fn, *args):
     """fn(*args, stream) on the first tensor's device and torch's current stream there."""
     torch = _torch()
@@ -624,7 +633,7 @@ def w4a16_attention(q, cache, block_table, lens, rows=None, scale=None, window=0
     _same_device(q, cache["k"], block_table, lens, rows, out, workspace)
     _launch(q, lib().w4a16_attention, q.data_ptr(), ldq, heads, ref, block_table.data_ptr(), width,
             lens.data_ptr(), _ptr(rows), B, T, c.dim ** -0.5 if scale is None else scale, window, out.data_ptr(),
-            _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size())
+            *_scratch(workspace))
     return out
 
 
@@ -665,6 +674,6 @@ def w4a16_decode_step_kv(stack, caches, block_table, lens, x, scale=None, out=No
             raise ValueError("out must be [M, H] = [%d, %d]" % tuple(x.shape))
     _same_device(x, block_table, lens, out, workspace, *[L["b_packed"] for L in stack], *[c["k"] for c in caches])
     _launch(x, lib().w4a16_decode_step_kv, lp, len(caches), cp, block_table.data_ptr(), width, lens.data_ptr(),
-            carr[0].dim ** -0.5 if scale is None else scale, x.data_ptr(), out.data_ptr(), M, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size())
+            carr[0].dim ** -0.5 if scale is None else scale, x.data_ptr(), out.data_ptr(), M,
+            *_scratch(workspace))
     return out

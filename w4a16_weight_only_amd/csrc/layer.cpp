@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <exception>
 #include <string>
 #include <utility>
 #include <vector>
@@ -329,21 +330,26 @@ int w4a16_decode_step_kv(const w4a16_linear *lin, int64_t n_layers, const w4a16_
         return fail(W4A16_ERR_UNSUPPORTED, "x_in, x_out and workspace must be 16-byte aligned");
     const Range x{x_in, (size_t)M * H * 2}, y{x_out, (size_t)M * H * 2}, ws{workspace, need};
     std::vector<std::pair<uintptr_t, uintptr_t>> spans;  // the caches' arrays
-    spans.reserve(4 * n_layers);
-    bool bad = overlaps(ws, x) || overlaps(ws, y) || (x_in != x_out && overlaps(x, y)) ||
-               overlaps(y, Range{block_table, (size_t)M * max_pages * 4}) || overlaps(y, Range{lens, (size_t)M * 4});
+    try {
+        spans.reserve(4 * n_layers);
+    } catch (const std::exception &) {
+        return fail(W4A16_ERR_INVALID_ARG, "no host memory to check the caches of so many layers");
+    }
+    const Range table{block_table, (size_t)M * max_pages * 4}, lengths{lens, (size_t)M * 4};
+    bool bad = overlaps(ws, x) || overlaps(ws, y) || (x_in != x_out && overlaps(x, y)) || overlaps(y, table) ||
+               overlaps(y, lengths) || overlaps(ws, table) || overlaps(ws, lengths);
     for (int64_t l = 0; l < n_layers; ++l) {
         const w4a16_kv_cache &k = caches[l];
         const size_t n = (size_t)k.pages * k.heads * k.page * k.dim, ns = (size_t)k.pages * k.heads;
         const Range parts[4] = {{k.k, n}, {k.v, n}, {k.k_scale, ns}, {k.v_scale, ns}};
         for (const Range &r : parts) {
-            bad = bad || overlaps(r, ws) || overlaps(r, x) || overlaps(r, y);
+            bad = bad || overlaps(r, ws) || overlaps(r, x) || overlaps(r, y) || overlaps(r, table) || overlaps(r, lengths);
             spans.emplace_back(reinterpret_cast<uintptr_t>(r.p), reinterpret_cast<uintptr_t>(r.p) + r.n);
         }
     }
     std::sort(spans.begin(), spans.end());
     for (size_t i = 1; i < spans.size(); ++i) bad = bad || spans[i].first < spans[i - 1].second;
-    if (bad) return fail(W4A16_ERR_INVALID_ARG, "x_in, x_out, workspace and the layers' caches must not overlap (x_out may be x_in)");
+    if (bad) return fail(W4A16_ERR_INVALID_ARG, "x_in, x_out, workspace, block_table, lens and the layers' caches must not overlap (x_out may be x_in)");
     // Buffers: P the linears' wide outputs, Q attention and glue scratch, R the
     // hidden rows between the linears.
     const size_t buf = three / 3;
