@@ -420,10 +420,13 @@ struct Place {
 
 // Few columns (single tokens): the workgroup's waves hold the same 16
 // columns and take chunks in turn, keys and values straight from memory into
-// registers.  Bound by reading the cache.  The loop is pipelined: a chunk's
-// keys are requested when those of the chunk before have been multiplied, its
-// values when those of the chunk before have; its pages are looked up one
-// chunk earlier still.
+// registers.  Bound by reading the cache: 48 sequences to 16384 tokens, 8 heads
+// of 128, 160 us for 811 MB (5.1 TB/s; a copy of 2 GiB reaches 4.9) and 6 us for
+// the join.  Short caches are bound by latency: one sequence of 64 tokens 5.4 us
+// in a graph, of 256 (a chunk for each wave) 6.9, 512 8.2, 1024 12.1.  The loop
+// is pipelined: a chunk's keys are requested when those of the chunk before have
+// been multiplied, its values when those of the chunk before have; its pages are
+// looked up one chunk earlier still.
 template <int D>
 __global__ __launch_bounds__(256, (D == 64 ? 3 : D == 128 ? 2 : 1)) void attention_token_kernel(Params p) {
     constexpr int W = 4;
@@ -556,7 +559,10 @@ __device__ __forceinline__ void load_to_lds16(const uint8_t *src, uint32_t to) {
 // the workgroup's 64 NT and all four walk the tile's chunks together.  A chunk
 // (64 tokens of K and of V, as stored) is staged in LDS once for the four, in
 // two buffers, by direct loads of whole lines; each wave converts what it reads
-// to fp16 in registers.
+// to fp16 in registers.  Bound by issuing vector instructions (conversions,
+// exponentials), 60% of the cycles against the matrix cores' 40%: four prompts,
+// the longest 4096 rows at 6001 tokens, 32 query heads over 8 of 128 dims, 616 us
+// (930 TFLOP/s; an fp16 product of 8192^3 reaches 1184).
 // LDS order: a token's keys are D / 16 pieces of 16 bytes, a dim's values four
 // (one per 16-token block); pieces are exchanged within their row so that the
 // eight lanes of a read phase, which want the same piece of different rows,
@@ -707,7 +713,8 @@ __global__ __launch_bounds__(256, (D <= 128 ? 2 : 1)) void attention_rows_kernel
 
 // Joins a column's pieces: one workgroup per column, D / 4 threads to a piece,
 // the 1024 / D groups of threads taking pieces in turn and meeting in LDS, in
-// order.
+// order.  48 sequences to 16384 tokens: 5.6 us, bound by launch and latency.  One
+// workgroup per tile left one sequence of 65536 at 61 us in both kernels, 29 now.
 template <int D>
 __global__ __launch_bounds__(256) void attention_join_kernel(Params p) {
     constexpr int TP = D / 4, GROUPS = 256 / TP;
@@ -795,7 +802,8 @@ AttnPlan plan_attention(int64_t heads, int64_t kv_heads, int64_t dim, int64_t pa
         // out ragged lengths), none where the tiles alone fill two.  Measured
         // on MI355X with 8 cache heads of 128: 48 sequences to 16384 tokens
         // 167 us (three pieces: 186), one of 65536 29 us, 128 of 2000 56 us
-        // (two pieces: 77).  A piece is at least a chunk for each wave, two
+        // (two pieces: 77); these with weights rounded once to fp16, as two
+        // values each 0 - 5% more on both sides.  A piece is at least a chunk for each wave, two
         // where there are more tiles: 4 of 2048 10.7 us (unsplit: 14.8), 8 of
         // 4096 16.7 us (pieces of four chunks: 18.2), 64 of 500 12.6 us
         // (23.5).  Up to 1024 tokens stay whole: the second launch costs what

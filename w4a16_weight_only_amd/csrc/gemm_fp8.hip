@@ -122,7 +122,10 @@ constexpr int64_t kTileMaxK = (int64_t)1 << 22;
 // LDS holds a row's 128 bytes of the block as eight 16-byte pieces, piece c at
 // place c ^ (row % 8), so the 16 rows a fragment read touches at one c cover
 // all banks; the direct load writes 1 KB (eight rows) per wave in lane order,
-// so the exchange is made in the lanes' global addresses.
+// so the exchange is made in the lanes' global addresses.  Measured with 256 x
+// 256 tiles at 8192^3: 513 us, 2140 TFLOP/s (a library product with one scale in
+// all: 2448), at 1.8 - 2.1 GHz; products, adds and barriers alone, without the
+// loads, take 445 us.
 template <int BM, int BN, int WM, int WN, int S, int KG>
 __global__ __launch_bounds__(64 * WM * WN * KG) void gemm_fp8_tile_kernel(const uint8_t *__restrict__ a,
                                                                       const float *__restrict__ sa,

@@ -17,7 +17,8 @@
 //
 // One workgroup owns one (page, head) of K or of V, so no two touch the same
 // scale: it reads the new rows for amax, again (from L2) to write codes.
-// Bound by HBM for prompts and by latency for single tokens.
+// Bound by HBM for prompts (12720 rows of 8 heads of 128: 20 us, 78 MB) and by a
+// chain of dependent loads (length, page, scale) for single tokens (64: 4.4 us).
 #include "device.h"
 #include "layer.h"
 

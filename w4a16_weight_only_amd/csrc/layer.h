@@ -75,7 +75,6 @@ hipError_t launch_attention(const uint16_t *q, int64_t ldq, int heads, const Cac
 
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 // 2^e for e in [-126, 127].
 __device__ __forceinline__ float pow2f(int e) { return __builtin_bit_cast(float, (uint32_t)(e + 127) << 23); }

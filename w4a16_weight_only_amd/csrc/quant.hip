@@ -8,7 +8,10 @@
 // Both are bound by HBM: each input is read once into registers and each
 // output written once.  The sum h stays in fp32 for the norm (its fp16
 // rounding is only the copy that the residual stream keeps), and so does y
-// until its one rounding, to fp16 or to e4m3.  A block of 128 columns is 16
+// until its one rounding, to fp16 or to e4m3.  Measured on MI355X: 8192 x 4096
+// to 8 bits 36 us (236 MB), SwiGLU of 4097 x 12800 36 us (264 MB), both above the
+// 4.9 TB/s of a 2 GiB copy, as the cache behind HBM holds part of them; three
+// rows 2.4 us, a launch and one load's latency.  A block of 128 columns is 16
 // lanes of 8, so its maximum is four lane exchanges inside a DPP row.
 #include "device.h"
 #include "layer.h"
