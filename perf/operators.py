@@ -8,8 +8,7 @@ heads of 128, QKV output 6144, MLP width 12800), and generic ones around them.
 
 Formulas (e4m3 is the OCP 8-bit format with a largest value of 448):
   append     cache page scale 2^e, e = clamp(ceil(log2(amax / 448)), -15, 8) over the page's tokens of one head (never
-             below the scale the page already had for earlier tokens); code = e4m3(x / 2^e), at most 240 at e = 8
-             (61440: every value the cache stands for is an fp16 value)
+             below the scale the page already had for earlier tokens); code = e4m3(x / 2^e)
   attention  out_i = sum_j softmax_j(scale * q_i . k_j) v_j over positions j <= pos_i (j > pos_i - window)
   norm       h = x + r;  y = w * h / sqrt(mean(h^2) + eps)
   quantise   t = x, or silu(x[:, :K]) * x[:, K:];  per row and block of 128: s = max(amax, 2^-40) / 448,
@@ -119,12 +118,7 @@ def _pages_of(x):
     """Quantises [pages, heads, page, dim] fp32 by page and head: codes and scale bytes."""
     amax = x.abs().amax(dim=(2, 3))
     byte = _scale_byte(amax)
-    return _codes(x, byte[:, :, None, None]), byte.to(torch.uint8)
-
-
-def _codes(x, byte):
-    most = torch.where(byte == 135, 240.0, 448.0)
-    return torch.minimum(torch.maximum(x / _pow2(byte), -most), most).to(FP8)
+    return (x / _pow2(byte)[:, :, None, None]).clamp(-448, 448).to(FP8), byte.to(torch.uint8)
 
 
 def _pow2(byte):
@@ -238,7 +232,7 @@ def _plain_append(s):
         again = (old * _pow2(127 + scale[head_page].int() - new[head_page])[:, :, None, None]).to(FP8).float()
         earlier = torch.arange(page, device="cuda")[None, None, :, None] < kept[:, None, None, None]
         rows[head_page] = torch.where(earlier, again, old).to(FP8)
-        rows[pid, :, at] = _codes(x, new[pid][:, :, None])
+        rows[pid, :, at] = (x / _pow2(new[pid])[:, :, None]).clamp(-448, 448).to(FP8)
         scale.copy_(new)
     return c["k"], c["v"], c["k_scale"], c["v_scale"]
 
