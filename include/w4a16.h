@@ -424,7 +424,8 @@ int w4a16_kv_append(const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t l
  *          may run at the same time; nothing in it need be initialised.
  * Scores and softmax are fp32; for the product with the values the weights are
  * rounded to fp16 where a sequence has many rows and heads, and carried as two
- * fp16 values where it has few (single tokens).  The order of the sums depends
+ * fp16 values where it has few (single tokens); either way weights below 2^-25
+ * of the row's largest are good to 2^-36 of it.  The order of the sums depends
  * on the sizes (B, T, max_pages) and lens alone, so results repeat bit for bit.
  * Errors: as for w4a16_kv_append; INVALID_ARG also for heads that are no
  * multiple of the cache's, a scale that is not finite, window < 0, a short

@@ -153,17 +153,21 @@ def cache_values(cache, pids, h):
     return K.reshape(-1, D), V.transpose(0, 2, 1).reshape(-1, D)
 
 
-def attention(q, cache, table, lens, rows, scale, window, out):
+def attention(q, cache, table, lens, rows, scale, window, out, parts=1):
     """Writes 64-bit results over `out` [T, heads * D] (other rows stay) and
     returns the error bound of fp32 scores and fp16 weights next to it:
 
-      weights   each is rounded to fp16: 2^-11 of it, or 2^-25 where it is below
-                fp16's normal range (weights are taken against a maximum that is
-                at least the first one seen, so their sum is at least 1);
+      weights   each is held as one fp16 value, 2^-11 of it, or with parts = 2
+                as two, 2^-22 of it, in the sum it is divided by as well; or,
+                where it is small, half of fp16's smallest step, 2^-25.
+                Weights stand 2^11 above their maximum's 1 (which is at most the
+                row's largest), so that is 2^-36;
       scores    D products summed in fp32, then one multiplication and one
                 subtraction: (D + 8) * 2^-24 of the magnitudes summed, twice over
                 for the weight and for the sum it is divided by; exp2 itself
                 2^-22;
+      sums      of n weights and weighted values, n * 2^-24 each at most (counted
+                with parts = 2; less than the weights' own roundings otherwise);
       output    one rounding to fp16: 2^-11, or 2^-25 absolute."""
     D, (P, H, page, _) = cache["k"].shape[3], cache["k"].shape
     heads = q.shape[1] // D
@@ -196,7 +200,8 @@ def attention(q, cache, table, lens, rows, scale, window, out):
                     l = p.sum()
                     out[r0 + i, col] = (p @ v) / l
                     mag = np.abs(scale) * (np.abs(k) @ np.abs(qi)).max() + np.abs(s).max()
-                    rel = 2.0 ** -11 + 2 * ((D + 8) * 2.0 ** -24 * mag + 2.0 ** -22)
+                    rel = 2.0 ** -11 if parts == 1 else 2.0 ** -21 + 2 * len(p) * 2.0 ** -24
+                    rel += 2 * ((D + 8) * 2.0 ** -24 * mag + 2.0 ** -22)
                     bound[r0 + i, col] = (2.0 ** -11 * np.abs(out[r0 + i, col]) + rel * (p @ np.abs(v)) / l +
-                                          len(p) * 2.0 ** -25 * np.nanmax(np.abs(v)) / l + 2.0 ** -25)
+                                          2 * len(p) * 2.0 ** -36 * np.nanmax(np.abs(v)) / l + 2.0 ** -25)
     return bound

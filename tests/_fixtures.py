@@ -7,6 +7,9 @@ import os
 
 import numpy as np
 
+from oracle import layer as lo
+from w4a16_weight_only_amd import synth
+
 GOLDEN = os.path.join(os.path.dirname(os.path.abspath(__file__)), "golden")
 
 
@@ -61,3 +64,24 @@ def oracle_gemm_columns(a, b_kn8, scales, qzeros, G, zp_bias=8):
     (identical to one oracle.gemm call)."""
     import oracle
     return oracle.gemm_columns(a, b_kn8, scales, qzeros, G, zp_bias)
+
+
+def sink_case(n, rows, gap, together):
+    """Keys that score about 0 but for one that stands `gap` above them, with values of zero there: every output is the
+    tail's.  Rows with gaps from gap - 8 to gap, in one sequence or each in its own over the same pages."""
+    D, page = 64, 64
+    g = synth.rng(n + rows)
+    pages = -(-n // page)
+    c = dict(k=np.zeros((pages, 1, page, D), np.uint8), v=np.zeros((pages, 1, D, page), np.uint8),
+             k_scale=np.full((pages, 1), 112, np.uint8), v_scale=np.full((pages, 1), 112, np.uint8))
+    k = (g.standard_normal((n, D)) * 0.05).astype(np.float16)
+    v = g.integers(1, 9, (n, D)).astype(np.float16)
+    k[:, 0] = 0
+    k[7], v[7] = 0, 0
+    k[7, 0] = 1
+    lo.kv_append(k, v, c, np.arange(pages)[None], [n], [0, n])
+    q = g.standard_normal((rows, D)).astype(np.float16)
+    q[:, 0] = np.linspace(gap - 8, gap, rows)
+    if together:
+        return q, c, np.arange(pages, dtype=np.int32)[None], np.array([n], np.int32), np.array([0, rows], np.int32)
+    return q, c, np.tile(np.arange(pages, dtype=np.int32), (rows, 1)), np.full(rows, n, np.int32), None

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from oracle import layer as lo
+from tests._fixtures import sink_case
 
 
 def test_e4m3_hand_values():
@@ -100,3 +101,35 @@ def test_append_grows_a_page_scale():
     K, V = lo.cache_values(c, [0], 0)
     assert np.array_equal(K[:2, 0], [1.0, 1024.0 if abs(1000 - 1024) < abs(1000 - 960) else 960.0])
     assert np.array_equal(V[:2, 0], [3.0, 0.5])
+
+
+def held(p, lift, parts):
+    """Weights p (the largest 1) as fp16 values 2^lift up, in one part or two."""
+    e = (p * 2.0 ** lift).astype(np.float32)
+    h = e.astype(np.float16)
+    low = (e - h.astype(np.float32)).astype(np.float16).astype(np.float64) if parts == 2 else 0.0
+    return h.astype(np.float64) + low
+
+
+def rebuilt(q, c, table, lens, off, lift, parts):
+    """Attention of one head with a scale of 1 over weights held in fp16, rounded to fp16 at the end."""
+    out = np.zeros(q.shape)
+    for b, (r0, n) in enumerate(lo.sequence_rows(off, lens)):
+        K, V = lo.cache_values(c, table[b], 0)
+        for i in range(n):
+            seen = int(lens[b]) - n + i + 1
+            s = K[:seen] @ q[r0 + i].astype(np.float64)
+            w = held(np.exp(s - s.max()), lift, parts)
+            out[r0 + i] = w @ V[:seen] / w.sum()
+    return out.astype(np.float16)
+
+
+@pytest.mark.parametrize("parts", [1, 2])
+def test_attention_bound_tells_a_lost_tail(parts):
+    """Weights that stand at 1 lose what lies 2^-25 below the largest, and the bound refuses that; 2^11 up they keep it."""
+    case = sink_case(3000, 12, 17.4, True)
+    want = np.zeros(case[0].shape)
+    bound = lo.attention(*case, 1.0, 0, want, parts=parts)
+    for lift, kept in ((0, False), (11, True)):
+        over = np.abs(rebuilt(*case, lift, parts) - want) / bound
+        assert (over.max() <= 1.0) == kept, (lift, over.max())

@@ -17,15 +17,17 @@
 // lane dequantises them: to fp16, exactly (kv_append.hip).
 //
 // Rounding: q and k are exact in fp16, their products summed in fp32; the
-// softmax runs in fp32.  For the second product prompts round P once to fp16
-// (2^-11 of each weight at most, as large as the result's own rounding; the
-// sums take the rounded weights too), at the rate of the matrix cores; single
-// tokens, bound by reading the cache, carry each weight as two fp16 values.
-// O and the sums of P are fp32 until the output.
+// softmax runs in fp32.  For the second product the row kernel rounds P once to
+// fp16 (2^-11 of each weight, as large as the result's own rounding; the sums
+// take the rounded weights too), at the rate of the matrix cores; the token
+// kernel, bound by reading the cache, carries each weight as two fp16 values
+// (2^-22 of it).  Either holds weights below 2^-25 of the row's largest to 2^-36
+// of that one (kLift).  O and the sums of P are fp32 until the output.  Two
+// values in the row kernel too: prompts of 4096 rows 850 us, 617 with one.
 //
 // The maximum a column's weights are taken against is raised only when some
-// score passes it by 2^8 (weights then stay below 2^8, far inside fp16), so
-// most chunks neither exchange maxima between lanes nor rescale O.
+// score passes it by 2^kLazy, so most chunks neither exchange maxima between
+// lanes nor rescale O.
 //
 // Splits: each (column tile, key/value head) is cut into pieces of `quota`
 // chunks, and with few columns the four waves of a workgroup take chunks in
@@ -40,7 +42,14 @@ namespace w4a16 {
 namespace {
 
 constexpr int kChunk = 64;
-constexpr float kLazy = 8.0f;  // in powers of two
+// In powers of two: how far a score may pass the running maximum before that is
+// raised, and how far above 1 a weight of the maximum itself stands.  Weights
+// stay below 2^(kLazy + kLift) = 2^15, inside fp16, and keep fp16's full
+// precision down to 2^-25 of the row's largest, the last of them at 2^-36: a row
+// with one dominant token and a long tail under it keeps the tail.
+// Measured: prompts of 4096 rows 617 us, 613 with 8 and no lift (tail lost at
+// 2^-25), 8 and 7 between the two; single tokens alike.
+constexpr float kLazy = 4.0f, kLift = 11.0f;
 
 struct Params {
     const uint16_t *q;
@@ -156,7 +165,8 @@ struct Pages {
 // NT tiles of 16 columns held by one wave: queries, running maxima, the sums of
 // the weights (one more row of O, from values of one) and O, all of it fp32.
 // FINE: weights enter the second product as two fp16 values, the second what
-// the first left over, so they are good to 2^-22.
+// the first left over: good to 2^-22, or where that is more to 2^-36 of the row's
+// largest.
 template <int D, int NT, bool FINE>
 struct Columns {
     static constexpr int PARTS = FINE ? 2 : 1;
@@ -290,7 +300,7 @@ struct Columns {
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const float base = mx[n] == -__builtin_inff() ? 0.f : mx[n] * scale;
+            const float base = mx[n] == -__builtin_inff() ? 0.f : max2(n);
 #pragma unroll
             for (int x = 0; x < 4; ++x)
 #pragma unroll
@@ -368,9 +378,10 @@ struct Columns {
         }
     }
 
-    // Maximum in powers of two, and sum, of this lane's column; NaN for a row
-    // longer than its table, and where every column saw a page out of range.
-    __device__ __forceinline__ float max2(int n) const { return mx[n] * scale; }
+    // What this lane's column takes weights against, in powers of two, and their
+    // sum; NaN for a row longer than its table, and where every column saw a page
+    // out of range.
+    __device__ __forceinline__ float max2(int n) const { return __builtin_fmaf(mx[n], scale, -kLift); }
     __device__ __forceinline__ float total(int n, int cap, bool lost) const {
         return lost || pos[n] >= cap ? __builtin_nanf("") : l[n][0];
     }
