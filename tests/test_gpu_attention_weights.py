@@ -1,4 +1,5 @@
-"""GPU checks of how attention holds its softmax weights: long tails under one dominant token.
+"""GPU checks of how attention holds its softmax weights: long tails under one dominant token, and scores
+far beyond fp32's whole numbers.
 
 Bounds are the oracle's, with each weight as one fp16 value (2^-11 of it) where a call has more than 16 rows and heads
 per sequence and key/value head on average, and as two (2^-22) otherwise.
@@ -8,7 +9,8 @@ import pytest
 
 from oracle import layer as lo
 from tests._fixtures import sink_case
-from tests.test_gpu_layer import check, gpu, run_attention  # noqa: F401  (gpu is a fixture)
+from tests.test_gpu_layer import attention_case, check, gpu, run_attention  # noqa: F401  (gpu is a fixture)
+from w4a16_weight_only_amd import synth
 
 pytestmark = pytest.mark.gpu
 
@@ -21,3 +23,27 @@ def test_tail_under_a_dominant_token(n, gap, rows, together):
     bound = lo.attention(q, c, table, lens, off, 1.0, 0, want, parts=1 if rows > 16 else 2)
     got, _, _ = run_attention(q, c, table, lens, off, 1.0)
     check(got, want, bound, "tail n=%d gap=%g rows=%d" % (n, gap, rows))
+
+
+@pytest.mark.parametrize("n,counts,width", [(300, [1], None), (3000, [1], 60), (300, [200], None), (300, [9], None)])
+@pytest.mark.parametrize("scale", [1.0, -1.0])
+def test_scores_beyond_whole_numbers(n, counts, width, scale):
+    """Scores of about 2^30, of which fp32 holds no fraction: the softmax picks each row's largest."""
+    D = 64
+    g = synth.rng(91)
+    q, c, table, lens, off = attention_case(g, [n], counts, 1, 1, D, 64, width=width)
+    k, v = (np.clip(g.standard_normal((n, D)) * f, -60000, 60000).astype(np.float16) for f in (16000, 1))
+    lo.kv_append(k, v, c, table, [n], [0, n])
+    q = np.clip(g.standard_normal(q.shape) * 16000, -60000, 60000).astype(np.float16)
+    got, _, _ = run_attention(q, c, table, lens, off, scale)
+    K, V = lo.cache_values(c, table[0, :-(-n // 64)], 0)
+    assert np.isfinite(got).all()
+    for i, row in enumerate(got):
+        seen = n - len(got) + i + 1
+        s = scale * (K[:seen] @ q[i].astype(np.float64))
+        first, second = np.sort(s)[:-3:-1]
+        # fp32 sums of D products are good to D 2^-24 of the magnitudes summed
+        apart = 2 * (D + 8) * 2.0 ** -24 * (np.abs(K[:seen]) @ np.abs(q[i].astype(np.float64))).max() + 40
+        assert first > 2.0 ** 28
+        if first - second > apart:
+            assert np.array_equal(row, V[s.argmax()].astype(np.float16)), "row %d" % i

@@ -50,6 +50,7 @@ constexpr int kChunk = 64;
 // Measured: prompts of 4096 rows 617 us, 613 with 8 and no lift (tail lost at
 // 2^-25), 8 and 7 between the two; single tokens alike.
 constexpr float kLazy = 4.0f, kLift = 11.0f;
+constexpr float kSteep = 0x1p20f;  // in powers of two; fp32 holds such a maximum to 2^-4
 
 struct Params {
     const uint16_t *q;
@@ -181,6 +182,7 @@ struct Columns {
     float mx[NT];  // of scores before their scale
     float scale, lazy;
     int window, hi;
+    bool steep;  // some column's maximum is kSteep or more: only masked chunks from here on
 
     // Columns wc0 .. wc0 + 16 NT of the tile's sequence.  Lane (c, g) holds
     // dims 64m + 16g .. + 15 of column c's query, the order in which keys come.
@@ -194,6 +196,7 @@ struct Columns {
         lazy = kLazy / scale;
         window = p.window;
         hi = t.hi;
+        steep = false;
         const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
         const int end = wc0 + 16 * NT < t.ncols ? wc0 + 16 * NT : t.ncols;
         pos_min = t.first + wc0 / p.group;
@@ -268,9 +271,14 @@ struct Columns {
                 }
     }
 
-    // Weights of a chunk, as fp16.  The running maxima are raised when
-    // a score passes them by kLazy after its scale.
-    __device__ __forceinline__ void weights(const f32x4 (&sc)[NT][4], f16x8 (&pf)[NT][PARTS][2]) {
+    // Weights of a chunk, as fp16.  The running maxima are raised when a score
+    // passes them by kLazy after its scale.  In CLEAN chunks a weight is one fma
+    // and exp2: the rounding of its base is common to the column and cancels, as
+    // long as the weights stay inside fp16.  Past kSteep they might not, so there,
+    // and in all other chunks, scores are taken from their maximum first.  (A
+    // branch on steep in every chunk instead: prompts of 4096 rows 643 us.)
+    template <bool CLEAN>
+    __device__ __forceinline__ void weights(f32x4 (&sc)[NT][4], f16x8 (&pf)[NT][PARTS][2]) {
         float top[NT];
         bool raise = false;
 #pragma unroll
@@ -282,7 +290,16 @@ struct Columns {
                 for (int i = 0; i < 4; ++i) top[n] = fmaxf(top[n], sc[n][x][i]);
             raise = raise || top[n] > mx[n] + lazy;
         }
+        auto from_maximum = [&]() __attribute__((always_inline)) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sc[n][x][i] -= mx[n] == -__builtin_inff() ? 0.f : mx[n];
+        };
         if (__any(raise)) {
+            bool far = false;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 top[n] = fmaxf(top[n], __shfl_xor(top[n], 16));
@@ -290,6 +307,7 @@ struct Columns {
                 const float m = fmaxf(mx[n], top[n]);
                 const float f = m == mx[n] ? 1.0f : __builtin_amdgcn_exp2f((mx[n] - m) * scale);
                 mx[n] = m;
+                far = far || (m != -__builtin_inff() && __builtin_fabsf(m * scale) >= kSteep);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) l[n][i] *= f;
 #pragma unroll
@@ -297,10 +315,15 @@ struct Columns {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o[n][d][i] *= f;
             }
+            if (__any(far)) {
+                steep = true;
+                if constexpr (CLEAN) from_maximum();
+            }
         }
+        if constexpr (!CLEAN) from_maximum();
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const float base = mx[n] == -__builtin_inff() ? 0.f : max2(n);
+            const float base = mx[n] == -__builtin_inff() ? 0.f : !CLEAN || steep ? -kLift : max2(n);
 #pragma unroll
             for (int x = 0; x < 4; ++x)
 #pragma unroll
@@ -398,7 +421,7 @@ struct Columns {
         scores(sc, key, fk);
         __builtin_amdgcn_s_setprio(0);
         if constexpr (!CLEAN) mask(sc, c, page_v == -2);
-        weights(sc, pf);
+        weights<CLEAN>(sc, pf);
         __builtin_amdgcn_s_setprio(1);
         values<CLEAN>(sc, pf, value, fv, page_v < 0 ? 0 : hi - (c * kChunk + 16 * (int)((threadIdx.x & 63) >> 4)));
         __builtin_amdgcn_s_setprio(0);
@@ -503,7 +526,7 @@ __global__ __launch_bounds__(256, (D == 64 ? 3 : D == 128 ? 2 : 1)) void attenti
             }
         }
         if constexpr (!decltype(clean)::value) cs.mask(sc, c, page_v == -2);
-        cs.weights(sc, pf);
+        cs.template weights<decltype(clean)::value>(sc, pf);
         cs.template values<decltype(clean)::value>(sc, pf, [&](int d) { return vr[d]; }, scale_of((uint8_t)bv),
                                                    page_v < 0 ? 0 : t.hi - (c * kChunk + 16 * g));
         if (more) load_values(c + W, pv_next);
@@ -515,7 +538,7 @@ __global__ __launch_bounds__(256, (D == 64 ? 3 : D == 128 ? 2 : 1)) void attenti
     int clean_lo, clean_hi;
     cs.clean_range(clo, chi, clean_lo, clean_hi);
     for (; c < clean_lo; c += W) turn(std::false_type{});
-    for (; c < clean_hi; c += W) turn(std::true_type{});
+    for (; c < clean_hi && !cs.steep; c += W) turn(std::true_type{});
     for (; c < chi; c += W) turn(std::false_type{});
 
     // The waves' pieces meet in LDS, in wave order.
@@ -694,7 +717,7 @@ __global__ __launch_bounds__(256, (D <= 128 ? 2 : 1)) void attention_rows_kernel
     if (!any_col) clean_lo = clean_hi = chi;
     int c = clo;
     for (; c < clean_lo; ++c) turn(c, std::false_type{});
-    for (; c < clean_hi; ++c) turn(c, std::true_type{});
+    for (; c < clean_hi && !cs.steep; ++c) turn(c, std::true_type{});
     for (; c < chi; ++c) turn(c, std::false_type{});
 
     if (!any_col) return;
