@@ -85,3 +85,19 @@ def sink_case(n, rows, gap, together):
     if together:
         return q, c, np.arange(pages, dtype=np.int32)[None], np.array([n], np.int32), np.array([0, rows], np.int32)
     return q, c, np.tile(np.arange(pages, dtype=np.int32), (rows, 1)), np.full(rows, n, np.int32), None
+
+
+def cancelling_case(B=64):
+    """Two tokens whose weighted values all but cancel: the output is what the weights' rounding leaves, far above its
+    own fp16 rounding."""
+    D, page = 64, 16
+    c = dict(k=np.zeros((B, 1, page, D), np.uint8), v=np.zeros((B, 1, D, page), np.uint8),
+             k_scale=np.full((B, 1), 112, np.uint8), v_scale=np.full((B, 1), 112, np.uint8))
+    k, v = np.zeros((2 * B, D), np.float16), np.ones((2 * B, D), np.float16)
+    k[1::2, 0] = 1
+    v[1::2] = -np.tile([1.125, 1.25, 1.375, 1.5], D // 4)
+    table, lens = np.arange(B, dtype=np.int32)[:, None], np.full(B, 2, np.int32)
+    lo.kv_append(k, v, c, table, lens, np.arange(0, 2 * B + 1, 2))
+    q = np.zeros((B, D), np.float16)
+    q[:, 0] = -np.log(np.tile([1.125, 1.25, 1.375, 1.5], B // 4)) + np.linspace(-1e-3, 1e-3, B)
+    return q, c, table, lens

@@ -1,5 +1,5 @@
-"""GPU checks of how attention holds its softmax weights: long tails under one dominant token, and scores
-far beyond fp32's whole numbers.
+"""GPU checks of how attention holds its softmax weights: long tails under one dominant token, scores far
+beyond fp32's whole numbers, and values that cancel.
 
 Bounds are the oracle's, with each weight as one fp16 value (2^-11 of it) where a call has more than 16 rows and heads
 per sequence and key/value head on average, and as two (2^-22) otherwise.
@@ -8,7 +8,7 @@ import numpy as np
 import pytest
 
 from oracle import layer as lo
-from tests._fixtures import sink_case
+from tests._fixtures import cancelling_case, sink_case
 from tests.test_gpu_layer import attention_case, check, gpu, run_attention  # noqa: F401  (gpu is a fixture)
 from w4a16_weight_only_amd import synth
 
@@ -47,3 +47,11 @@ def test_scores_beyond_whole_numbers(n, counts, width, scale):
         assert first > 2.0 ** 28
         if first - second > apart:
             assert np.array_equal(row, V[s.argmax()].astype(np.float16)), "row %d" % i
+
+
+def test_single_tokens_carry_their_weights_in_two_parts():
+    q, c, table, lens = cancelling_case()
+    want = np.zeros(q.shape)
+    bound = lo.attention(q, c, table, lens, None, 1.0, 0, want, parts=2)
+    got, _, _ = run_attention(q, c, table, lens, None, 1.0)
+    check(got, want, bound, "cancelling")

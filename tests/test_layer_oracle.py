@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from oracle import layer as lo
-from tests._fixtures import sink_case
+from tests._fixtures import cancelling_case, sink_case
 
 
 def test_e4m3_hand_values():
@@ -133,3 +133,12 @@ def test_attention_bound_tells_a_lost_tail(parts):
     for lift, kept in ((0, False), (11, True)):
         over = np.abs(rebuilt(*case, lift, parts) - want) / bound
         assert (over.max() <= 1.0) == kept, (lift, over.max())
+
+
+def test_attention_bound_tells_weights_of_one_part_from_two():
+    q, c, table, lens = cancelling_case()
+    want = np.zeros(q.shape)
+    bound = lo.attention(q, c, table, lens, None, 1.0, 0, want, parts=2)
+    for parts in (1, 2):
+        over = np.abs(rebuilt(q, c, table, lens, None, 11, parts) - want) / bound
+        assert (over.max() <= 1.0) == (parts == 2), (parts, over.max())
