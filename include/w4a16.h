@@ -423,10 +423,12 @@ int w4a16_kv_append(const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t l
  *          (NULL where that is 0), caller-owned, not shared with a call that
  *          may run at the same time; nothing in it need be initialised.
  * Scores and softmax are fp32; for the product with the values the weights are
- * rounded to fp16 where a sequence has many rows and heads, and carried as two
- * fp16 values where it has few (single tokens); either way weights below 2^-25
+ * carried as two fp16 values each where a call's sequences have few rows (single
+ * tokens: at most 16 rows times query heads to a cache head, T * heads /
+ * (B * cache->heads)), and rounded once to fp16 in all other calls, in which
+ * single tokens may share a call with prompts.  Either way weights below 2^-25
  * of the row's largest are good to 2^-36 of it.  The order of the sums depends
- * on the sizes (B, T, max_pages) and lens alone, so results repeat bit for bit.
+ * on the sizes, lens, rows and window alone, so results repeat bit for bit.
  * Errors: as for w4a16_kv_append; INVALID_ARG also for heads that are no
  * multiple of the cache's, a scale that is not finite, window < 0, a short
  * workspace, or out or workspace overlapping anything else; UNSUPPORTED for

@@ -1,5 +1,5 @@
 """GPU checks of how attention holds its softmax weights: long tails under one dominant token, scores far
-beyond fp32's whole numbers, and values that cancel.
+beyond fp32's whole numbers, values that cancel, and calls that mix prompts with single tokens.
 
 Bounds are the oracle's, with each weight as one fp16 value (2^-11 of it) where a call has more than 16 rows and heads
 per sequence and key/value head on average, and as two (2^-22) otherwise.
@@ -55,3 +55,18 @@ def test_single_tokens_carry_their_weights_in_two_parts():
     bound = lo.attention(q, c, table, lens, None, 1.0, 0, want, parts=2)
     got, _, _ = run_attention(q, c, table, lens, None, 1.0)
     check(got, want, bound, "cancelling")
+
+
+@pytest.mark.parametrize("lens,counts", [([3000, 700, 40], [1, 60, 1]), ([900] * 6 + [64], [1] * 6 + [40]), ([900] * 6 + [64], [1] * 6 + [12]),
+                                         ([2, 2000, 130], [2, 1, 130])])
+@pytest.mark.parametrize("window", [0, 100])
+def test_prompts_beside_single_tokens(lens, counts, window):
+    """One call over both, single tokens over long caches among them.  All of it is held as the call's average sequence is:
+    up to 16 rows and heads to a key/value head in two fp16 values per weight, else in one."""
+    g = synth.rng(97)
+    q, c, table, lens, off = attention_case(g, lens, counts, 2, 4, 64, 32, extra_rows=2, heavy=True, width=100)
+    few = -(-len(q) * 4 // len(lens)) <= 16
+    want = np.full(q.shape, -77.0)
+    bound = lo.attention(q, c, table, lens, off, 0.125, window, want, parts=2 if few else 1)
+    got, _, _ = run_attention(q, c, table, lens, off, 0.125, window)
+    check(got, want, np.where(bound == 0, 1e-30, bound), "mixed")
