@@ -1,6 +1,9 @@
 """Refusals of the decoder-layer operators, at the C ABI and the Python binding (no GPU: every call here is rejected,
 or returns as a no-op, before any HIP call)."""
 import ctypes
+import glob
+import os
+import re
 
 import pytest
 import torch
@@ -246,3 +249,14 @@ def test_python_binding_refuses(lib):  # noqa: F811
     assert w4._scratch(None) == (None, 0) and w4._scratch(x)[1] == 1024
     with pytest.raises(ValueError, match="contiguous"):
         w4._scratch(x[:, ::2])
+
+
+def test_inline_assembly_declares_what_it_writes():
+    """Every block that sets m0 tells the compiler so, and every block that loads names memory."""
+    blocks = []
+    for path in glob.glob(os.path.join(os.path.dirname(w4.__file__), "csrc", "*")):
+        with open(path) as f:
+            blocks += re.findall(r"\basm\s+volatile\s*\((.*?)\);\n", f.read(), re.S)
+    setters = [b for b in blocks if "s_mov_b32 m0" in b]
+    assert setters and all('"m0"' in b.rsplit(":", 1)[1] for b in setters)
+    assert all('"memory"' in b.rsplit(":", 1)[1] for b in blocks if "_load_" in b)

@@ -586,7 +586,7 @@ __global__ __launch_bounds__(256, (D == 64 ? 3 : D == 128 ? 2 : 1)) void attenti
 // Requests 16 bytes per lane from `src` into LDS at `to` + 16 * lane; there is
 // no register result, and the kernel waits for its loads itself.
 __device__ __forceinline__ void load_to_lds16(const uint8_t *src, uint32_t to) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(src) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(src) : "memory", "m0");
 }
 
 // Many columns (prompts): wave w holds columns [w * 16 NT, (w + 1) * 16 NT) of

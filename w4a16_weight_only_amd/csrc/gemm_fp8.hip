@@ -98,12 +98,12 @@ __global__ __launch_bounds__(64 * kRowWaves) void gemm_fp8_row_kernel(const uint
 __device__ __forceinline__ void load_to_lds16(u32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t to) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(to), "v"(voff), "s"(rsrc),
                  "s"(soff)
-                 : "memory");
+                 : "memory", "m0");
 }
 __device__ __forceinline__ void load_to_lds4(u32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t to) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(to), "v"(voff), "s"(rsrc),
                  "s"(soff)
-                 : "memory");
+                 : "memory", "m0");
 }
 // Waits until at most N of the wave's loads are still on their way, and its LDS
 // reads are done.
