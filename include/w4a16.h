@@ -455,9 +455,11 @@ int w4a16_attention(const uint16_t *q, int64_t ldq, int64_t heads, const w4a16_k
  *                w4a16_gemm_glue(RMSNORM, R, H, gate_up)      -> P
  *                w4a16_gemm_glue(SWIGLU, P, 2I, down)         -> R
  *     then       w4a16_rownorm(R, H, M, H)                    -> x_out
- *   caches  host array of n_layers caches, apart in memory; block_table and
- *           lens (with this token) are shared by the layers and lie outside
- *           the caches and the workspace.
+ *   caches  host array of n_layers caches; block_table and lens (with this
+ *           token) are shared by the layers.
+ * What the step writes (x_out, the workspace, the caches) may overlap nothing
+ * else, but x_out may be x_in; layers may share weights.  All of it is checked
+ * before the first launch.
  * Errors: as for w4a16_decode_step, w4a16_kv_append and w4a16_attention.
  */
 size_t w4a16_decode_kv_workspace_bytes(int64_t M, const w4a16_linear *lin, int64_t n_layers,

@@ -221,6 +221,18 @@ def test_decode_step_kv_rejects(lib, kw, status):  # noqa: F811
     assert lib.w4a16_last_error().decode() != ""
 
 
+@pytest.mark.parametrize("kw", [
+    dict(ws=W + 0x100_0000 * 5), dict(ws=W + 0x100_0000 * 7 + 64), dict(ws=S + 0x100_0000), dict(y=W + 0x100_0000 * 4),
+    dict(y=S + 0x100_0000 * 7), dict(weights=KC + 0x2000),
+])
+def test_decode_step_kv_rejects_written_memory_over_weights(lib, kw):  # noqa: F811
+    """Before anything is launched: a step refused half way would have written its tokens to some of the caches."""
+    stack, kw = _stack(), dict(kw)
+    stack[6].b_packed = kw.pop("weights", stack[6].b_packed)
+    assert step(lib, stack=stack, **kw) == INVALID
+    assert "overlap" in lib.w4a16_last_error().decode()
+
+
 def test_decode_step_kv_workspace(lib):  # noqa: F811
     s, c = ctypes.cast(_stack(), ctypes.c_void_p), ctypes.cast(_caches(), ctypes.c_void_p)
     three = lib.w4a16_decode_workspace_bytes(3, s, 2)

@@ -8,7 +8,6 @@
 #include <cmath>
 #include <exception>
 #include <string>
-#include <utility>
 #include <vector>
 
 #include "kernels.h"
@@ -46,6 +45,11 @@ bool clash(std::initializer_list<Range> outs, std::initializer_list<Range> ins) 
     }
     return false;
 }
+
+struct Span {
+    uintptr_t begin, end;
+    bool written;
+};
 
 Range rows_range(const void *p, int64_t rows, int64_t ld, int64_t width) {
     return Range{p, rows > 0 ? (size_t)((rows - 1) * ld + width) * 2 : 0};
@@ -328,28 +332,45 @@ int w4a16_decode_step_kv(const w4a16_linear *lin, int64_t n_layers, const w4a16_
         return fail(W4A16_ERR_UNSUPPORTED, "decode step too large for 32-bit kernel indexing");
     if (!aligned16(x_in) || !aligned16(x_out) || !aligned16(workspace))
         return fail(W4A16_ERR_UNSUPPORTED, "x_in, x_out and workspace must be 16-byte aligned");
-    const Range x{x_in, (size_t)M * H * 2}, y{x_out, (size_t)M * H * 2}, ws{workspace, need};
-    std::vector<std::pair<uintptr_t, uintptr_t>> spans;  // the caches' arrays
+    // Everything the step touches, in the order of its addresses: what it writes
+    // may overlap nothing, what it only reads may (layers that share weights).
+    std::vector<Span> spans;
     try {
-        spans.reserve(4 * n_layers);
+        spans.reserve(16 * (size_t)n_layers + 5);
     } catch (const std::exception &) {
-        return fail(W4A16_ERR_INVALID_ARG, "no host memory to check the caches of so many layers");
+        return fail(W4A16_ERR_INVALID_ARG, "no host memory to check the memory of so many layers");
     }
-    const Range table{block_table, (size_t)M * max_pages * 4}, lengths{lens, (size_t)M * 4};
-    bool bad = overlaps(ws, x) || overlaps(ws, y) || (x_in != x_out && overlaps(x, y)) || overlaps(y, table) ||
-               overlaps(y, lengths) || overlaps(ws, table) || overlaps(ws, lengths);
+    auto span = [&](const void *p, size_t n, bool written) {
+        if (p && n) spans.push_back(Span{reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + n, written});
+    };
+    if (x_in != x_out) span(x_in, (size_t)M * H * 2, false);
+    span(x_out, (size_t)M * H * 2, true);
+    span(workspace, need, true);
+    span(block_table, (size_t)M * max_pages * 4, false);
+    span(lens, (size_t)M * 4, false);
     for (int64_t l = 0; l < n_layers; ++l) {
         const w4a16_kv_cache &k = caches[l];
         const size_t n = (size_t)k.pages * k.heads * k.page * k.dim, ns = (size_t)k.pages * k.heads;
-        const Range parts[4] = {{k.k, n}, {k.v, n}, {k.k_scale, ns}, {k.v_scale, ns}};
-        for (const Range &r : parts) {
-            bad = bad || overlaps(r, ws) || overlaps(r, x) || overlaps(r, y) || overlaps(r, table) || overlaps(r, lengths);
-            spans.emplace_back(reinterpret_cast<uintptr_t>(r.p), reinterpret_cast<uintptr_t>(r.p) + r.n);
+        span(k.k, n, true);
+        span(k.v, n, true);
+        span(k.k_scale, ns, true);
+        span(k.v_scale, ns, true);
+        for (int j = 0; j < 4; ++j) {
+            const w4a16_linear &L = lin[4 * l + j];
+            span(L.b_packed, (size_t)L.K * L.N / 2, false);
+            span(L.scales, (size_t)(L.K / L.G) * L.N * 2, false);
+            span(L.qzeros, (size_t)(L.K / L.G) * L.N / 2, false);
         }
     }
-    std::sort(spans.begin(), spans.end());
-    for (size_t i = 1; i < spans.size(); ++i) bad = bad || spans[i].first < spans[i - 1].second;
-    if (bad) return fail(W4A16_ERR_INVALID_ARG, "x_in, x_out, workspace, block_table, lens and the layers' caches must not overlap (x_out may be x_in)");
+    std::sort(spans.begin(), spans.end(), [](const Span &a, const Span &b) { return a.begin < b.begin; });
+    uintptr_t any_end = 0, written_end = 0;  // of the spans so far
+    for (const Span &a : spans) {
+        if (a.begin < (a.written ? any_end : written_end))
+            return fail(W4A16_ERR_INVALID_ARG, "x_in, x_out, workspace, block_table, lens, the layers' caches and their "
+                                               "weights must not overlap (x_out may be x_in)");
+        any_end = std::max(any_end, a.end);
+        if (a.written) written_end = std::max(written_end, a.end);
+    }
     // Buffers: P the linears' wide outputs, Q attention and glue scratch, R the
     // hidden rows between the linears.
     const size_t buf = three / 3;
