@@ -263,6 +263,19 @@ def test_python_binding_refuses(lib):  # noqa: F811
         w4._scratch(x[:, ::2])
 
 
+def test_python_binding_checks_the_stacks_scales():
+    """The library reads K/G rows of N scales from an address; a smaller tensor there would be read past its end."""
+    def linear(scales, qzeros=None, G=32):
+        return dict(b_packed=torch.zeros(128, 16, dtype=torch.int32), scales=torch.zeros(scales, dtype=torch.float16),
+                    qzeros=None if qzeros is None else torch.zeros(qzeros, dtype=torch.int32), G=G, zp_bias=8)
+
+    w4._check_linear_shapes([linear((4, 128)), linear((4, 128), (4, 16))])
+    for bad in (linear((3, 128)), linear((4, 120)), linear((4, 128), (4, 15)), linear((4, 128), (1, 16)),
+                linear((4, 128), G=64), linear((4, 128), G=0)):
+        with pytest.raises(ValueError, match="linear 1"):
+            w4._check_linear_shapes([linear((4, 128)), bad])
+
+
 def test_inline_assembly_declares_what_it_writes():
     """Every block that sets m0 tells the compiler so, and every block that loads names memory."""
     blocks = []

@@ -637,12 +637,25 @@ def w4a16_attention(q, cache, block_table, lens, rows=None, scale=None, window=0
     return out
 
 
+def _check_linear_shapes(stack):
+    """Scales and zeros of the size the kernels read (the library sees only their addresses)."""
+    for i, L in enumerate(stack):
+        (K, words), G, qz = L["b_packed"].shape, L["G"], L.get("qzeros")
+        groups = K // G if G > 0 else 0
+        if tuple(L["scales"].shape) != (groups, words * 8):
+            raise ValueError("scales of linear %d must be [K/G, N] = [%d, %d], got %s"
+                             % (i, groups, words * 8, tuple(L["scales"].shape)))
+        if qz is not None and tuple(qz.shape) != (groups, words):
+            raise ValueError("qzeros of linear %d must be [K/G, N/8] = [%d, %d], got %s" % (i, groups, words, tuple(qz.shape)))
+
+
 def _decode_kv_args(stack, caches, M, max_pages):
     if len(stack) % 4 != 0 or not stack:
         raise ValueError("stack must hold 4 linears per layer")
     if len(caches) != len(stack) // 4:
         raise ValueError("caches must hold one cache per layer")
     arr = _linear_array(stack)
+    _check_linear_shapes(stack)
     carr = (KVCache * len(caches))(*[_cache_struct(c) for c in caches])
     lp, cp = ctypes.cast(arr, ctypes.c_void_p), ctypes.cast(carr, ctypes.c_void_p)
     need = int(lib().w4a16_decode_kv_workspace_bytes(M, lp, len(caches), cp, max_pages))
@@ -672,7 +685,8 @@ def w4a16_decode_step_kv(stack, caches, block_table, lens, x, scale=None, out=No
         _dev_tensor(out, "out", torch.float16, 2)
         if out.shape != x.shape:
             raise ValueError("out must be [M, H] = [%d, %d]" % tuple(x.shape))
-    _same_device(x, block_table, lens, out, workspace, *[L["b_packed"] for L in stack], *[c["k"] for c in caches])
+    _same_device(x, block_table, lens, out, workspace, *[t for L in stack for t in (L["b_packed"], L["scales"], L.get("qzeros"))],
+                 *[c["k"] for c in caches])
     _launch(x, lib().w4a16_decode_step_kv, lp, len(caches), cp, block_table.data_ptr(), width, lens.data_ptr(),
             carr[0].dim ** -0.5 if scale is None else scale, x.data_ptr(), out.data_ptr(), M,
             *_scratch(workspace))
