@@ -353,7 +353,10 @@ int w4a16_gemm_fp8(const uint8_t *a, const float *a_scales, const uint8_t *b, co
                    int64_t K, int64_t N, uint16_t *out, hipStream_t stream);
 
 /* The workgroup tile (rows x cols of out) and the number of wave groups that
- * divide K which w4a16_gemm_fp8 takes for a size (host-only, no HIP calls).
+ * divide K which w4a16_gemm_fp8 takes for a size (host-only, no HIP calls).  Where
+ * the largest tiles would leave a last round of the chip mostly empty, the
+ * product runs as two launches along N: this is the first one's, the second takes
+ * what a product of its own columns would.
  * Returns what w4a16_gemm_fp8 would return for the sizes alone. */
 int w4a16_gemm_fp8_plan(int64_t M, int64_t K, int64_t N, int32_t *rows, int32_t *cols, int32_t *groups);
 

@@ -534,7 +534,7 @@ def w4a16_gemm_fp8(a, a_scales, b, b_scales, out=None):
 
 def w4a16_gemm_fp8_plan(M, K, N):
     """(rows, cols, groups): the workgroup tile and the wave groups dividing K that
-    w4a16_gemm_fp8 takes for a size."""
+    w4a16_gemm_fp8 takes for a size (of its first launch, where it needs two)."""
     r, c, g = ctypes.c_int32(), ctypes.c_int32(), ctypes.c_int32()
     _check(lib().w4a16_gemm_fp8_plan(M, K, N, ctypes.byref(r), ctypes.byref(c), ctypes.byref(g)))
     return r.value, c.value, g.value

@@ -595,7 +595,7 @@ __device__ __forceinline__ void load_to_lds16(const uint8_t *src, uint32_t to) {
 // two buffers, by direct loads of whole lines; each wave converts what it reads
 // to fp16 in registers.  Bound by issuing vector instructions (conversions,
 // exponentials), 60% of the cycles against the matrix cores' 40%: four prompts,
-// the longest 4096 rows at 6001 tokens, 32 query heads over 8 of 128 dims, 616 us
+// the longest 4096 rows at 6001 tokens, 32 query heads over 8 of 128 dims, 620 us
 // (930 TFLOP/s; an fp16 product of 8192^3 reaches 1184).
 // LDS order: a token's keys are D / 16 pieces of 16 bytes, a dim's values four
 // (one per 16-token block); pieces are exchanged within their row so that the
@@ -819,8 +819,8 @@ AttnPlan plan_attention(int64_t heads, int64_t kv_heads, int64_t dim, int64_t pa
     p.shared = per <= 16;
     // Two column tiles per wave share each conversion of keys and values; one
     // gives twice the workgroups.  Measured on MI355X: 2000 rows after 6000
-    // tokens (504 workgroups with two) 271 us, 337 with one; 1000 rows (256)
-    // 35 us, 29 with one.
+    // tokens (504 workgroups with two) 255 us, 328 with one; 1500 rows (376) 51
+    // us, 43 with one; 1000 rows (256) 34 us, 28 with one.
     p.nt = 1;
     if (!p.shared && per > 64 && dim < 256 && (T * group / 128 + B) * kv_heads >= 400) p.nt = 2;
     p.cols = p.shared ? 16 : 64 * p.nt;
@@ -834,22 +834,26 @@ AttnPlan plan_attention(int64_t heads, int64_t kv_heads, int64_t dim, int64_t pa
     if (p.shared) {
         // Pieces to about 2048 workgroups (four rounds of the chip, which evens
         // out ragged lengths), none where the tiles alone fill two.  Measured
-        // on MI355X with 8 cache heads of 128: 48 sequences to 16384 tokens
-        // 167 us (three pieces: 186), one of 65536 29 us, 128 of 2000 56 us
-        // (two pieces: 77); these with weights rounded once to fp16, as two
-        // values each 0 - 5% more on both sides.  A piece is at least a chunk for each wave, two
-        // where there are more tiles: 4 of 2048 10.7 us (unsplit: 14.8), 8 of
-        // 4096 16.7 us (pieces of four chunks: 18.2), 64 of 500 12.6 us
-        // (23.5).  Up to 1024 tokens stay whole: the second launch costs what
-        // it saves (one of 777 10.1 us against 11.8 in a graph, 14.2 against
-        // 12 launched one by one).
+        // on MI355X with 8 cache heads of 128 and a table as wide as the longest
+        // sequence: 48 sequences to 16384 tokens 166 us (half as many pieces
+        // 185, twice as many 162), one of 65536 29 us, 128 of 2000 59 us (two
+        // pieces: 78); 72 of 3000 (576 tiles) 67 us, 51 whole, so the border
+        // could lie lower.  A piece is at least a chunk for each wave, two
+        // where there are more tiles: 4 of 2048 10.8 us (whole: 20.9), 8 of 4096
+        // 17.0 us (pieces of four chunks: 18.5, whole: 41), 64 of 500 13.3 us
+        // (pieces of four chunks: 23.7).  Up to 1024 tokens stay whole: a second
+        // launch and its workspace cost 4 us of host time where calls are
+        // launched one by one (one of 777: 12.8 us, 16.6 in pieces; one of 1024:
+        // 12.6 and 17.4) and save 2.5 where they are replayed from a graph (12.7
+        // and 10.2; 12.6 and 10.0).
         splits = wgs >= 1024 ? 1 : (2048 + wgs - 1) / wgs;
         least = wgs >= 64 ? 8 : chunks <= 16 ? 16 : 4;
     } else {
         // A piece of a prompt writes and reads back far more than it saves
-        // once the tiles come near to filling the chip: 1000 rows (264
-        // workgroups) 29 us whole, 80 in two pieces; 128 rows after 3872
-        // tokens (72) 33 us in seven pieces, 74 whole.
+        // once the tiles come near to filling the chip: 1000 rows (504
+        // workgroups) 28 us whole, 78 in two pieces; 400 rows after 1600 tokens
+        // (208) 45 us whole, 56 in two; 128 rows after 3872 (72) 34 us in seven
+        // pieces, 78 whole.
         splits = wgs >= 192 ? 1 : (512 + wgs - 1) / wgs;
         least = 8;
     }

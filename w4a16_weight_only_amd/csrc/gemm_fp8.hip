@@ -390,8 +390,9 @@ int choose(int64_t M, int64_t K, int64_t N, double *us) {
 // Columns of the first of two launches: where the largest tiles' last round
 // would leave most CUs idle, the columns of the whole rounds come first and the
 // rest takes the shape of its own size.  N: one launch.  Measured with K = 4096
-// N = 25600: M = 4096 (6.25 rounds) 510 -> 500 us, M = 2048 (3.1 rounds) 314 ->
-// 283 us; less than the rounds saved, as fewer busy CUs run at higher clocks.
+// N = 25600: M = 4096 (6.25 rounds) 490 us in one launch, 465 in two, M = 2048 (3.1
+// rounds) 273 and 238; less than the rounds saved, as fewer busy CUs run at higher
+// clocks.
 int64_t first_columns(int64_t M, int64_t K, int64_t N, int shape, double us) {
     const TileShape &s = kShapes[sizeof(kShapes) / sizeof(kShapes[0]) - 1];
     if (shape != (int)(sizeof(kShapes) / sizeof(kShapes[0])) - 1) return N;
