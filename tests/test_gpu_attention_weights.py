@@ -49,6 +49,32 @@ def test_scores_beyond_whole_numbers(n, counts, width, scale):
             assert np.array_equal(row, V[s.argmax()].astype(np.float16)), "row %d" % i
 
 
+@pytest.mark.parametrize("n,counts,width", [(700, [1], None), (3000, [1], 60), (700, [500], None), (700, [9], None)])
+def test_scores_that_grow_beyond_whole_numbers(n, counts, width):
+    """Small scores, then ones of 2^17, of 2^24 and of 2^30 along the cache: rows that end among the first follow the
+    softmax, the others pick their largest."""
+    D = 64
+    g = synth.rng(93)
+    q, c, table, lens, off = attention_case(g, [n], counts, 1, 1, D, 64, width=width)
+    size = np.repeat([0.002, 2.0, 250.0, 16000.0], -(-n // 4))[:n, None]
+    k, v = (np.clip(g.standard_normal((n, D)) * f, -60000, 60000).astype(np.float16) for f in (size, 1))
+    lo.kv_append(k, v, c, table, [n], [0, n])
+    q = np.clip(g.standard_normal(q.shape) * 16000, -60000, 60000).astype(np.float16)
+    q[:n // 4] *= np.float16(0.01)
+    got, want, bound = run_attention(q, c, table, lens, off, 1.0)
+    check(got, want, bound, "growing")
+    K, V = lo.cache_values(c, table[0, :-(-n // 64)], 0)
+    picked = 0
+    for i, row in enumerate(got):
+        seen = n - len(got) + i + 1
+        s = K[:seen] @ q[i].astype(np.float64)
+        first, second = np.sort(s)[:-3:-1]
+        if first - second > 2 * (D + 8) * 2.0 ** -24 * (np.abs(K[:seen]) @ np.abs(q[i].astype(np.float64))).max() + 40:
+            assert np.array_equal(row, V[s.argmax()].astype(np.float16)), "row %d" % i
+            picked += 1
+    assert picked > 0
+
+
 def test_single_tokens_carry_their_weights_in_two_parts():
     q, c, table, lens = cancelling_case()
     want = np.zeros(q.shape)
