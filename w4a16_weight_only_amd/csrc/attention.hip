@@ -19,11 +19,12 @@
 // Rounding: q and k are exact in fp16, their products summed in fp32; the
 // softmax runs in fp32.  For the second product the row kernel rounds P once to
 // fp16 (2^-11 of each weight, as large as the result's own rounding; the sums
-// take the rounded weights too), at the rate of the matrix cores; the token
-// kernel, bound by reading the cache, carries each weight as two fp16 values
-// (2^-22 of it).  Either holds weights below 2^-25 of the row's largest to 2^-36
-// of that one (kLift).  O and the sums of P are fp32 until the output.  Two
-// values in the row kernel too: prompts of 4096 rows 850 us, 617 with one.
+// take the rounded weights too, so that a row stays a mean of its values), at
+// the rate of the matrix cores.  The token kernel, bound by reading the cache,
+// carries each weight as two fp16 values (2^-22 of it).  Either holds weights
+// below 2^-25 of the row's largest to 2^-36 of that one (kLift).  O and the sums
+// of P are fp32 until the output.  Two values in the row kernel too: prompts of
+// 4096 rows 850 us, 617 with one.
 //
 // The maximum a column's weights are taken against is raised only when some
 // score passes it by 2^kLazy, so most chunks neither exchange maxima between
